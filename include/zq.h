@@ -273,6 +273,162 @@ zq_status zq_gemm_w8a8_noalloc(const int8_t* Xq, const float* s_tok, const int8_
                                void* Y, int32_t* acc_dbg, zq_stream_t stream);
 
 /*
+ * Block-scaled FP8: the quantized linear layer with e4m3 codes on both sides
+ * and one fp32 scale for each 128 values of an activation row and for each
+ * 128 x 128 block of a weight matrix.  Where the INT8 forms above give a
+ * whole token row (or a whole group of weight rows) one scale, an outlier
+ * here costs resolution only inside its own block.
+ *
+ * Types of the 16-bit tensors of these calls (the calls above take fp16).
+ */
+typedef enum { ZQ_F16 = 0, ZQ_BF16 = 1 } zq_dtype;
+
+/*
+ * Quantization of one block, shared by the calls below: with amax the largest
+ * magnitude in the block (of fp32 values) and a = max(amax, 2^-110),
+ *   scale = a / 448,   code = e4m3(y * (448 / a)),
+ * the division rounded once, the code rounded to nearest even from a product
+ * whose relative error is at most 2^-24 and which is exact where the quotient
+ * lies exactly between two codes.  An all-zero block has scale 0 and codes 0.
+ * A block with Inf or NaN in it has scale Inf or NaN and NaN codes, so that
+ * it shows in every output that it reaches.
+ *
+ * Blocks start at multiples of 128; the last one of a row (or of the weight
+ * rows) is shorter when K (or N) is no multiple of 128.  KB = ceil(K/128),
+ * NB = ceil(N/128).
+ */
+
+/*
+ * zq_quantize_weights_fp8 -- weights to e4m3 with 128 x 128 blocks.
+ *   W      fp16 or bf16 (`dtype`) [N][K].
+ *   Wq     e4m3 [N][K] output; s_blk fp32 [NB][KB] output.
+ * Requirements: N >= 1, K >= 16, K % 16 == 0, W and Wq 16-byte aligned,
+ * s_blk 4-byte aligned.
+ */
+zq_status zq_quantize_weights_fp8(const void* W, int dtype, int N, int K, void* Wq, float* s_blk,
+                                  zq_stream_t stream);
+
+/*
+ * zq_ln_quant_fp8 -- fused LayerNorm + e4m3 quantization of token rows.
+ *   X, gamma, beta   fp16 or bf16 (`dtype`), as zq_ln_quant: gamma NULL
+ *          quantizes x itself, beta NULL = 0.
+ *          y = ((x - mean) * rstd) * gamma + beta in fp32, from the mean and
+ *          the centred sum of squares of the row (fp32, read once).
+ *   Xq     e4m3 [T][K], s_blk fp32 [T][KB]: y quantized without a rounding
+ *          to 16 bits in between.
+ *   Y_ln   [T][K] of `dtype` or NULL: also store y.
+ * Requirements: T >= 0 (T == 0 is a no-op), 16 <= K <= 32768, K % 16 == 0,
+ * pointers 16-byte aligned (s_blk 4-byte).
+ */
+zq_status zq_ln_quant_fp8(const void* X, int dtype, const void* gamma, const void* beta, int T,
+                          int K, float eps, void* Xq, float* s_blk, void* Y_ln,
+                          zq_stream_t stream);
+
+/*
+ * zq_bias_act_quant_fp8 -- e4m3 quantization fused into a bias-add or a GeLU:
+ *   v = f32(x) + f32(bias) (bias NULL: v = x), y = v or gelu(v) in fp32 (act
+ *   as zq_bias_act_quant), quantized without a rounding in between.
+ *   X, bias, Y_act   of `dtype`; outputs as zq_ln_quant_fp8.
+ * Requirements: as zq_ln_quant_fp8.
+ */
+zq_status zq_bias_act_quant_fp8(const void* X, int dtype, const void* bias, int T, int K, int act,
+                                void* Xq, float* s_blk, void* Y_act, zq_stream_t stream);
+
+/*
+ * zq_gemm_fp8 -- the linear layer on block-scaled e4m3 codes.
+ *   Xq, s_x   e4m3 [T][K], fp32 [T][KB] (zq_ln_quant_fp8, zq_bias_act_quant_fp8).
+ *   Wq, s_w   e4m3 [N][K], fp32 [NB][KB] (zq_quantize_weights_fp8).
+ *   bias      [N] of `dtype` or NULL (= 0).
+ *   Y         [T][N] of `dtype` (ZQ_F16 or ZQ_BF16):
+ *     Y[t][o] = sum over b < KB of (s_x[t][b] * s_w[o / 128][b]) * d[t][o][b] + bias[o],
+ *     d[t][o][b] = sum over the k of block b of xq[t][k] * wq[o][k].
+ *     d is summed by the tensor cores in fp32; the blocks are added in fp32,
+ *     in an order that the sizes alone set (the same inputs give the same
+ *     bits); one rounding to `dtype` at the end.
+ * No workspace: calls on different streams, and replayed graphs of them, may
+ * overlap.
+ * Requirements: T >= 0 (T == 0 is a no-op), N >= 8, N % 8 == 0,
+ * 16 <= K <= 2^20, K % 16 == 0, pointers 16-byte aligned (scales 4-byte).
+ * ZQ_OPT_GEMM_PATH forces a kernel: 1 = the tensor-memory tiles, 2 = weight
+ * streaming (other values: ZQ_ERR_UNSUPPORTED).
+ */
+zq_status zq_gemm_fp8(const void* Xq, const float* s_x, const void* Wq, const float* s_w,
+                      const void* bias, int T, int N, int K, int dtype, void* Y,
+                      zq_stream_t stream);
+
+/*
+ * zq_qk_norm_rope -- the step between a QKV projection and attention: the
+ * norm of each query and key head (or none) and the rotation of its first R
+ * values by the token's position, in one pass over both.
+ *   q, k       host pointers to the description of the query and key heads;
+ *              k may be NULL.  `in` and `out` point at head 0 of token 0, of
+ *              `dtype`; value d of head h of token t is at
+ *              t * token_stride + h * head_stride + d (strides in elements).
+ *              out == in (with equal strides) works in place; other overlaps
+ *              of in and out are not allowed.
+ *   norm       ZQ_NORM_NONE, ZQ_NORM_RMS (x / sqrt(mean(x^2) + eps)) or
+ *              ZQ_NORM_LAYER ((x - mean) / sqrt(var + eps)) over the D values
+ *              of a head, then weight[d] (NULL = 1) and bias[d] (NULL = 0);
+ *              in fp32.  Without a norm weight and bias are ignored.
+ *   positions  int32 [T]; a token whose position is negative (padding behind
+ *              the last sequence) is neither read nor written.
+ *   inv_freq   fp32 [R/2] on the device, radians per position
+ *              (zq_rope_frequencies).
+ *   layout     ZQ_ROPE_HALF pairs values i and i + R/2 (GPT-NeoX),
+ *              ZQ_ROPE_INTERLEAVED 2i and 2i + 1 (GPT-J), with frequency i.
+ *              (a, b) -> (a cos - b sin, b cos + a sin) * scale; the angle
+ *              position * inv_freq[i] is reduced in 64 bits, so far positions
+ *              are as exact as near ones.
+ *   Values behind R get the norm alone.
+ * Requirements: T >= 0, 8 <= D <= 256, D % 8 == 0, 0 <= R <= D, R even
+ * (R % 4 == 0 for ZQ_ROPE_HALF), head counts >= 0, strides >= 0 and multiples
+ * of 8, output heads that do not overlap (all heads of a token before the
+ * next token, or all tokens of a head before the next head), tensor pointers
+ * 16-byte aligned, positions and inv_freq 4-byte.
+ */
+typedef enum { ZQ_NORM_NONE = 0, ZQ_NORM_RMS = 1, ZQ_NORM_LAYER = 2 } zq_norm;
+typedef enum { ZQ_ROPE_HALF = 0, ZQ_ROPE_INTERLEAVED = 1 } zq_rope_layout;
+typedef struct {
+  const void* in;
+  void* out;
+  const void* weight;
+  const void* bias;
+  long long in_token_stride, in_head_stride, out_token_stride, out_head_stride;
+  int heads;
+} zq_heads;
+zq_status zq_qk_norm_rope(const zq_heads* q, const zq_heads* k, int dtype, int T, int D, int norm,
+                          float eps, const int32_t* positions, const float* inv_freq, int R,
+                          int layout, float scale, zq_stream_t stream);
+
+/*
+ * zq_rope_frequencies -- the R/2 frequencies of a rotation and the factor on
+ * its cosine and sine, into HOST memory (no GPU work).  f_i = base^(-2i/R),
+ * computed in 64 bits and rounded once, then for contexts `factor` times
+ * longer than the model was trained on:
+ *   ZQ_ROPE_PLAIN    f_i (factor, low, high, trained_len ignored)
+ *   ZQ_ROPE_LINEAR   f_i / factor (positions interpolated)
+ *   ZQ_ROPE_NTK      base * factor^(R/(R-2)) in place of base (R > 2)
+ *   ZQ_ROPE_BANDS    by the turns that a frequency makes over trained_len:
+ *                    kept from `high` turns on, divided by factor below `low`,
+ *                    a linear blend of both between
+ *   ZQ_ROPE_YARN     the same blend over the index i, between the indices
+ *                    (rounded outwards) at which f_i makes `high` and `low`
+ *                    turns; *scale = 0.1 ln(factor) + 1
+ * *scale is 1 for the others.
+ * Requirements: 2 <= R <= 256, R even, base > 1, factor >= 1, and for the last
+ * two 0 < low < high and trained_len >= 1.
+ */
+typedef enum {
+  ZQ_ROPE_PLAIN = 0,
+  ZQ_ROPE_LINEAR = 1,
+  ZQ_ROPE_NTK = 2,
+  ZQ_ROPE_BANDS = 3,
+  ZQ_ROPE_YARN = 4
+} zq_rope_scaling;
+zq_status zq_rope_frequencies(int R, double base, int scaling, double factor, double low,
+                              double high, int trained_len, float* inv_freq, float* scale);
+
+/*
  * zq_device_status -- synchronize `stream`, then read and clear the status
  * word of the current device.  Returns ZQ_OK, ZQ_ERR_TIMEOUT when a kernel
  * gave up a bounded wait since the last call (*detail receives the kernel's

@@ -25,8 +25,18 @@ EXPORTS = (
     "zq_gemm_w8a8", "zq_gemm_w4a8", "zq_device_status", "zq_set_option", "zq_get_option",
     "zq_debug_wait_timeout", "zq_gemm_w8a8_noalloc", "zq_bias_act_quant", "zq_static_quant",
     "zq_gemm_w8a16", "zq_gemm_w4a16", "zq_launch_count", "zq_workspace_reserve",
-    "zq_widen_int4_weights",
+    "zq_widen_int4_weights", "zq_quantize_weights_fp8", "zq_ln_quant_fp8", "zq_bias_act_quant_fp8",
+    "zq_gemm_fp8", "zq_qk_norm_rope", "zq_rope_frequencies",
 )
+
+
+class Heads(ctypes.Structure):
+    """zq_heads: query or key heads in a strided tensor."""
+
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("in_token_stride", ctypes.c_longlong),
+                ("in_head_stride", ctypes.c_longlong), ("out_token_stride", ctypes.c_longlong),
+                ("out_head_stride", ctypes.c_longlong), ("heads", ctypes.c_int)]
 
 
 class ZQError(RuntimeError):
@@ -60,6 +70,14 @@ def _load():
         "zq_launch_count": ([], ctypes.c_ulonglong),
         "zq_workspace_reserve": ([ctypes.c_ulonglong], I),
         "zq_widen_int4_weights": ([P, I, I, P, P], I),
+        "zq_quantize_weights_fp8": ([P, I, I, I, P, P, P], I),
+        "zq_ln_quant_fp8": ([P, I, P, P, I, I, F, P, P, P, P], I),
+        "zq_bias_act_quant_fp8": ([P, I, P, I, I, I, P, P, P, P], I),
+        "zq_gemm_fp8": ([P, P, P, P, P, I, I, I, I, P, P], I),
+        "zq_qk_norm_rope": ([ctypes.POINTER(Heads), ctypes.POINTER(Heads), I, I, I, I, F, P, P, I,
+                             I, F, P], I),
+        "zq_rope_frequencies": ([I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double,
+                                 ctypes.c_double, I, ctypes.POINTER(F), ctypes.POINTER(F)], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -291,6 +309,181 @@ def gemm_w4a16(X, Wq4, s_grp, bias=None, Y=None, acc_dbg=None, stream=None):
     """As gemm_w8a16 with packed INT4 weights uint8 [N, K/2]."""
     return _gemm_a16(_lib.zq_gemm_w4a16, "zq_gemm_w4a16", X, Wq4, s_grp, bias, Wq4.shape[0], Y,
                      acc_dbg, stream, 4)
+
+
+# ------------------------------------------------- block-scaled FP8 (e4m3)
+
+FP8 = torch.float8_e4m3fn
+FP8_BLOCK = 128
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # zq_dtype
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def _dtype16(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    return d
+
+
+def _same_device(*tensors):
+    """The kernels run on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got {t.device}")
+
+
+def quantize_weights_fp8(W: torch.Tensor, Wq=None, s_blk=None, stream=None):
+    """Weights [N,K] (fp16 or bf16) to e4m3 with one scale for each 128 x 128
+    block (zq_quantize_weights_fp8).  Returns (Wq float8_e4m3fn [N,K],
+    s_blk fp32 [ceil(N/128), ceil(K/128)])."""
+    N, K = W.shape
+    dt = _dtype16(W, "W")
+    w = _dev(W, W.dtype, (N, K), "W")
+    if Wq is None:
+        Wq = torch.empty((N, K), dtype=FP8, device=W.device)
+    blocks = (_blocks(N), _blocks(K))
+    if s_blk is None:
+        s_blk = torch.empty(blocks, dtype=torch.float32, device=W.device)
+    args = (w, dt, N, K, _dev(Wq, FP8, (N, K), "Wq"), _dev(s_blk, torch.float32, blocks, "s_blk"))
+    _same_device(W, Wq, s_blk)
+    _check(_lib.zq_quantize_weights_fp8(*args, _stream(stream)), "zq_quantize_weights_fp8")
+    return Wq, s_blk
+
+
+def _fp8_rows(X, Xq, s_blk):
+    T, K = X.shape
+    if Xq is None:
+        Xq = torch.empty((T, K), dtype=FP8, device=X.device)
+    blocks = (T, _blocks(K))
+    if s_blk is None:
+        s_blk = torch.empty(blocks, dtype=torch.float32, device=X.device)
+    return T, K, Xq, s_blk, _dev(Xq, FP8, (T, K), "Xq"), _dev(s_blk, torch.float32, blocks, "s_blk")
+
+
+def ln_quant_fp8(X: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, Xq=None, s_blk=None,
+                 y_ln=None, stream=None):
+    """Fused LayerNorm + e4m3 quantization of token rows with one scale for
+    each 128 values (zq_ln_quant_fp8); gamma=None is quant-only.  X, gamma,
+    beta and y_ln share one dtype, fp16 or bf16.  Returns (Xq float8_e4m3fn
+    [T,K], s_blk fp32 [T, ceil(K/128)])."""
+    dt = _dtype16(X, "X")
+    x = _dev(X, X.dtype, tuple(X.shape), "X")
+    T, K, Xq, s_blk, xq, sb = _fp8_rows(X, Xq, s_blk)
+    args = (x, dt, _dev(gamma, X.dtype, (K,), "gamma"), _dev(beta, X.dtype, (K,), "beta"), T, K,
+            float(eps), xq, sb, _dev(y_ln, X.dtype, (T, K), "Y_ln"))
+    _same_device(X, gamma, beta, Xq, s_blk, y_ln)
+    _check(_lib.zq_ln_quant_fp8(*args, _stream(stream)), "zq_ln_quant_fp8")
+    return Xq, s_blk
+
+
+def bias_act_quant_fp8(X: torch.Tensor, bias=None, act: int = ACT_NONE, Xq=None, s_blk=None, y=None,
+                       stream=None):
+    """e4m3 quantization of token rows fused into a bias-add (act=ACT_NONE) or
+    a bias-add and GeLU (act=ACT_GELU) (zq_bias_act_quant_fp8).  Returns as
+    ln_quant_fp8; y, if given, receives the activation."""
+    dt = _dtype16(X, "X")
+    x = _dev(X, X.dtype, tuple(X.shape), "X")
+    T, K, Xq, s_blk, xq, sb = _fp8_rows(X, Xq, s_blk)
+    args = (x, dt, _dev(bias, X.dtype, (K,), "bias"), T, K, int(act), xq, sb,
+            _dev(y, X.dtype, (T, K), "Y_act"))
+    _same_device(X, bias, Xq, s_blk, y)
+    _check(_lib.zq_bias_act_quant_fp8(*args, _stream(stream)), "zq_bias_act_quant_fp8")
+    return Xq, s_blk
+
+
+def gemm_fp8(Xq, s_x, Wq, s_w, bias=None, Y=None, out_dtype=torch.float16, stream=None):
+    """Y = (s_x Xq) (s_w Wq)^T + bias on block-scaled e4m3 codes
+    (zq_gemm_fp8); Y and bias are of out_dtype, fp16 or bf16."""
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"out_dtype must be torch.float16 or torch.bfloat16, got {out_dtype}")
+    T, K = Xq.shape
+    N = Wq.shape[0]
+    if Y is None:
+        Y = torch.empty((T, N), dtype=out_dtype, device=Xq.device)
+    kb = _blocks(K)
+    args = (_dev(Xq, FP8, (T, K), "Xq"), _dev(s_x, torch.float32, (T, kb), "s_x"),
+            _dev(Wq, FP8, (N, K), "Wq"), _dev(s_w, torch.float32, (_blocks(N), kb), "s_w"),
+            _dev(bias, out_dtype, (N,), "bias"), T, N, K, _DTYPES[out_dtype],
+            _dev(Y, out_dtype, (T, N), "Y"))
+    _same_device(Xq, s_x, Wq, s_w, bias, Y)
+    _check(_lib.zq_gemm_fp8(*args, _stream(stream)), "zq_gemm_fp8")
+    return Y
+
+
+# ------------------------------------------- query/key norm and rotation
+
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
+
+
+def rope_frequencies(R: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                     low: float = 1.0, high: float = 32.0, trained_len: int = 0):
+    """Frequencies of a rotation of R values and the factor on its cosine and
+    sine (zq_rope_frequencies; host only).  Returns (inv_freq fp32 [R/2] on the
+    CPU, scale): move inv_freq to the device once and keep it."""
+    f = (ctypes.c_float * max(1, R // 2))()
+    scale = ctypes.c_float(0.0)
+    _check(_lib.zq_rope_frequencies(int(R), float(base), int(scaling), float(factor), float(low),
+                                    float(high), int(trained_len), f, ctypes.byref(scale)),
+           "zq_rope_frequencies")
+    return torch.tensor(list(f), dtype=torch.float32), float(scale.value)
+
+
+def _heads(t, out, weight, bias, T, D, dtype, name):
+    """(zq_heads, out) of a strided [T, heads, D] tensor."""
+    for what, v in ((name, t), (name + "_out", out)):
+        if v is None:
+            continue
+        if not isinstance(v, torch.Tensor) or not v.is_cuda:
+            raise TypeError(f"{what} must be a CUDA tensor")
+        if v.dtype != dtype:
+            raise TypeError(f"{what} must be {dtype}, got {v.dtype}")
+        if v.dim() != 3 or v.shape[0] != T or v.shape[1] != t.shape[1] or v.shape[2] != D:
+            raise ValueError(f"{what} must have shape ({T}, {t.shape[1]}, {D}), got {tuple(v.shape)}")
+        if D > 1 and v.stride(2) != 1:
+            raise ValueError(f"the values of a head of {what} must be contiguous")
+    if out is None:
+        out = torch.empty(t.shape, dtype=dtype, device=t.device)
+    # strides of dimensions of one element mean nothing and may be anything
+    st = [0 if v.shape[d] <= 1 else v.stride(d) for v in (t, out) for d in (0, 1)]
+    h = Heads(t.data_ptr(), out.data_ptr(), _dev(weight, dtype, (D,), name + "_weight"),
+              _dev(bias, dtype, (D,), name + "_bias"), *st, t.shape[1])
+    return h, out
+
+
+def qk_norm_rope(q, k, positions, inv_freq, layout: int = ROPE_HALF, scale: float = 1.0,
+                 norm: int = NORM_NONE, eps: float = 1e-6, q_weight=None, q_bias=None, k_weight=None,
+                 k_bias=None, q_out=None, k_out=None, stream=None):
+    """Norm of each query and key head and its rotation by position
+    (zq_qk_norm_rope).  q [T, Hq, D] and k [T, Hk, D] (or None) are fp16 or
+    bf16 with contiguous heads and any token and head strides that are
+    multiples of 8, e.g. slices of a fused QKV output.  positions int32 [T] on
+    the device (negative: the row is skipped), inv_freq fp32 [R/2] (R values of
+    a head are rotated).  q_out=q works in place; without q_out a new tensor is
+    made (its skipped rows are undefined).  Returns (q_out, k_out)."""
+    dt = _dtype16(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must have shape (tokens, heads, head_dim), got {tuple(q.shape)}")
+    T, _, D = q.shape
+    hq, q_out = _heads(q, q_out, q_weight, q_bias, T, D, q.dtype, "q")
+    hk = None
+    if k is not None:
+        hk, k_out = _heads(k, k_out, k_weight, k_bias, T, D, q.dtype, "k")
+    half = inv_freq.shape[0]
+    args = (dt, T, D, int(norm), float(eps), _dev(positions, torch.int32, (T,), "positions"),
+            _dev(inv_freq, torch.float32, (half,), "inv_freq"), 2 * half, int(layout), float(scale))
+    _same_device(q, k, positions, inv_freq, q_weight, q_bias, k_weight, k_bias, q_out, k_out)
+    _check(_lib.zq_qk_norm_rope(ctypes.byref(hq), None if hk is None else ctypes.byref(hk), *args,
+                                _stream(stream)), "zq_qk_norm_rope")
+    return q_out, k_out
 
 
 def debug_wait_timeout(stream=None):
