@@ -8,6 +8,7 @@
 // then scaled and added in fp32 registers.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "zq_fp8.cuh"
 #include "zq_internal.h"
@@ -26,123 +27,442 @@ struct Fp8Params {
   int T, N, K, kblocks;
 };
 
-// --------------------------------------------------------- weight streaming
-//
-// A few tokens: the weights' bytes bound the call, and each is used once, so
-// they go from global memory straight into the registers that mma.sync reads
-// as its 16 x 32 A operand (8 tokens are the B operand).  The sum over k does
-// not care about the order of k, so a lane takes 16 consecutive bytes of its
-// row where the instruction's layout names four pieces of four, and the same
-// bytes of the token rows.  The warps of a CTA share 16 weight rows and take
-// every eighth block of 128 k each; their sums are added in warp order.
-constexpr int kStreamWarps = 8;
-constexpr int kStreamRows = 16;
-constexpr int kStreamMaxTokens = 32;
-
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Every lane waits (bounded); true when all of them saw the phase complete.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         int* status, int site) {
+  const bool ok = mbar_wait(bar, parity, abort, status, site);
+  return __all_sync(0xffffffffu, ok);
 }
 
-template <typename E, int NT>
-__global__ void __launch_bounds__(32 * kStreamWarps) fp8_stream_kernel(const Fp8Params p) {
-  __shared__ float part[kStreamWarps][8 * NT][kStreamRows];
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
+  asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tfma.rn.f32x2 %0, d, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(s));
+}
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+// Raises a kernel's dynamic shared-memory limit once per device.
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (ready.load() >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
+  return e;
+}
+
+// ------------------------------------------------------------ weight rows
+//
+// Up to 128 tokens: the weights' bytes bound the call, so they have to flow
+// without a pause.  A CTA has R weight rows (the 128-row operand of its
+// MMAs; rows past R are never looked at) and TN token
+// columns, streamed through a deep ring of 128-k slices by TMA.  The MMAs of
+// a block write their own columns of an accumulator buffer in tensor memory;
+// eight warps take BATCH blocks at a time from there and add them up in fp32
+// registers, a lane per weight row and a factor per column:
+// acc[c] += d[c] * (s_x[t(c)][b] * s_w[nb][b]).  (One block at a time, the
+// waits and tensor-memory loads of a block took 650 cycles: more than its
+// copy where R is small.)
+//
+// R is chosen so that one wave of CTAs covers the weights.  Where that would
+// leave a CTA few rows (and so little to copy per block), the CTAs of a
+// cluster share rows along K and exchange their sums through distributed
+// shared memory: rank r ends with every token c with c mod S == r, added in
+// rank order.
+constexpr int kRowsMaxTokens = 64;
+constexpr int kRowsAccWarps = 8;
+constexpr int kRowsThreads = 32 * (4 + kRowsAccWarps);  // copies, MMAs, scales (two warps)
+constexpr int kRowsMaxStages = 16;
+// Two CTAs fit an SM: their waits and ends overlap, and the next call's
+// set-up and first copies to L2 overlap the end of this one.
+constexpr int kRowsSmem = 112 * 1024;
+
+template <int TN_>
+struct RowsCfg {
+  static constexpr int TN = TN_;        // token columns
+  static constexpr int COLS = TN / 2;   // of an accumulating warp
+  static constexpr int CHUNK = COLS < 32 ? COLS : 32;  // columns of one TMEM load
+  // scale blocks per accumulator buffer: as many as a warp has 32 columns for
+  static constexpr int BATCH = COLS >= 32 ? 1 : 32 / COLS;
+  static constexpr int BUF_COLS = BATCH * TN;
+  static constexpr int NBUF = 512 / BUF_COLS > 4 ? 4 : 512 / BUF_COLS;
+  static constexpr int TMEM_COLS = BUF_COLS * NBUF;
+  static_assert(2 * TMEM_COLS <= 512, "tensor memory of two CTAs");
+  static_assert(TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory allocation");
+  // blocks whose scales travel together, and floats of such a slot: the
+  // tokens' [block][token], then the weights' [row block][block]
+  static constexpr int G = TN <= 32 ? 32 : 16;
+  static constexpr int SX_ROW = TN + 4;
+  static constexpr int W_BLOCKS = 2;  // weight blocks that R rows can touch
+  static constexpr int SLOT = G * SX_ROW + W_BLOCKS * G;
+};
+
+struct RowsParams {
+  const float* s_x;
+  const float* s_w;
+  const void* bias;
+  void* Y;
+  int* status;
+  int T, N, kblocks;
+  int rows, stages, stage_bytes;
+  int off_slots, off_xchg;  // shared memory, from the aligned base
+};
+
+template <typename E, class C>
+__global__ void __launch_bounds__(kRowsThreads, 2)
+    fp8_rows_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
+                         const __grid_constant__ CUtensorMap map_w, const RowsParams p) {
+  constexpr int NBUF = C::NBUF, COLS = C::COLS, CHUNK = C::CHUNK, G = C::G;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full_bar[kRowsMaxStages], empty_bar[kRowsMaxStages], tfull_bar[NBUF],
+      tempty_bar[NBUF], sfull_bar[2], sempty_bar[2], drain_bar;
+  __shared__ uint32_t tmem_holder;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int S = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+  const int o_cta = static_cast<int>(blockIdx.x) / S * p.rows;
+  const int kb0 = static_cast<int>(static_cast<long long>(p.kblocks) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<long long>(p.kblocks) * (rank + 1) / S);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tempty_bar[b], kRowsAccWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sfull_bar[b], 2);
+      mbar_init(&sempty_bar[b], kRowsAccWarps);
+    }
+    mbar_init(&drain_bar, 1);
+    abort_word = 0;
+    fence_mbar_init();
+    // The first weight slices may go on their way to L2 before the previous
+    // kernel of the stream has finished: only L2 is touched, which that
+    // kernel's writes reach coherently.
+    for (int kb = kb0; kb < min(kb1, kb0 + p.stages); ++kb)
+      tma_prefetch_l2_2d(&map_w, kb * kFp8Block, o_cta);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_holder, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (S > 1) cluster_sync_all();  // all CTAs of the cluster are there before any remote use
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_holder;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int g = lane >> 2, q = lane & 3;
-  const int o0 = blockIdx.x * kStreamRows, t0 = blockIdx.y * 8 * NT;
-  const uint8_t* wlo = p.Wq + static_cast<size_t>(o0 + g) * p.K;
-  const uint8_t* whi = wlo + static_cast<size_t>(8) * p.K;
-  const bool lo_ok = o0 + g < p.N, hi_ok = o0 + g + 8 < p.N;
-  const float* sw = p.s_w + static_cast<size_t>(o0 / kFp8Block) * p.kblocks;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
 
-  struct Block {
-    uint4 lo[2], hi[2], x[NT][2];
-    float sx[NT][2], sw;
-  };
-  auto fetch = [&](int kb, Block& f) {
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, p.status, 51)) break;
+        uint8_t* dst = smem + stage * p.stage_bytes;
+        mbar_arrive_expect_tx(&full_bar[stage], p.stage_bytes);
+        tma_load_2d(dst, &map_w, &full_bar[stage], kb * kFp8Block, o_cta, pol_w);
+        tma_load_2d(dst + p.rows * kFp8Block, &map_x, &full_bar[stage], kb * kFp8Block, 0, pol_x);
+        ++issued;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // every copy issued has landed before the CTA goes on
+      int no_abort = 0;
+      for (int s = 0; s < min(p.stages, issued); ++s)
+        mbar_wait(&full_bar[s], ((issued - 1 - s) / p.stages) & 1, &no_abort, p.status, 52);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc = make_idesc_e4m3(128, C::TN);
+    const bool leader = elect_one();
+    const uint64_t desc0 = make_sw128_desc(smem_u32(smem));
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, tphase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int b = (kb - kb0) % C::BATCH;
+      const bool last = b == C::BATCH - 1 || kb + 1 == kb1;  // of the buffer
+      if (!wait_all(&full_bar[stage], phase, abort_flag, p.status, 53) ||
+          (b == 0 && !wait_all(&tempty_bar[buf], tphase ^ 1, abort_flag, p.status, 54)))
+        break;
+      tc_fence_after();
+      const uint64_t da = desc0 + static_cast<uint64_t>(stage * (p.stage_bytes >> 4));
+      const uint64_t db = da + static_cast<uint64_t>(p.rows * kFp8Block >> 4);
+      if (leader) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = kb * kFp8Block + h * 64 + q * 16;
-      const bool in = k < p.K;
-      f.lo[h] = lo_ok && in ? __ldcs(reinterpret_cast<const uint4*>(wlo + k)) : zero;
-      f.hi[h] = hi_ok && in ? __ldcs(reinterpret_cast<const uint4*>(whi + k)) : zero;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int t = t0 + 8 * n + g;
-        f.x[n][h] = t < p.T && in ? __ldg(reinterpret_cast<const uint4*>(
-                                        p.Xq + static_cast<size_t>(t) * p.K + k))
-                                  : zero;
+        for (int k = 0; k < kFp8Block / 32; ++k)  // 32 bytes further in the swizzle row: +2
+          mma_f8(tmem_base + static_cast<uint32_t>(buf * C::BUF_COLS + b * C::TN), da + 2 * k,
+                 db + 2 * k, idesc, k > 0);
+        mma_commit(&empty_bar[stage]);
+        if (last) mma_commit(&tfull_bar[buf]);
+      }
+      __syncwarp();
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (last && ++buf == NBUF) {
+        buf = 0;
+        tphase ^= 1;
       }
     }
-    f.sw = __ldg(sw + kb);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = t0 + 8 * n + 2 * q + j;
-        f.sx[n][j] = t < p.T ? __ldg(p.s_x + static_cast<size_t>(t) * p.kblocks + kb) : 0.0f;
-      }
-  };
-  float acc[NT][4] = {};
-  Block cur;
-  if (warp < p.kblocks) fetch(warp, cur);
-  for (int kb = warp; kb < p.kblocks; kb += kStreamWarps) {
-    Block next;
-    if (kb + kStreamWarps < p.kblocks) fetch(kb + kStreamWarps, next);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float d[4] = {};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mma_e4m3(d, cur.lo[h].x, cur.hi[h].x, cur.lo[h].y, cur.hi[h].y, cur.x[n][h].x,
-                 cur.x[n][h].y);
-        mma_e4m3(d, cur.lo[h].z, cur.hi[h].z, cur.lo[h].w, cur.hi[h].w, cur.x[n][h].z,
-                 cur.x[n][h].w);
-      }
-      const float s0 = cur.sx[n][0] * cur.sw, s1 = cur.sx[n][1] * cur.sw;
-      acc[n][0] = fmaf(d[0], s0, acc[n][0]);  // row g, tokens 2q and 2q + 1
-      acc[n][1] = fmaf(d[1], s1, acc[n][1]);
-      acc[n][2] = fmaf(d[2], s0, acc[n][2]);  // row g + 8
-      acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+    // all MMAs of this thread are done before tensor memory is freed
+    if (leader) {
+      mma_commit(&drain_bar);
+      int no_abort = 0;
+      mbar_wait(&drain_bar, 0, &no_abort, p.status, 55);
     }
-    cur = next;
-  }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------ scales
+    // The two warps take half of the tokens each; a lane reads one of G
+    // neighbouring scales of every (32 / G)th token, all in flight together.
+    constexpr int PER_LANE = C::TN / 2 * G / 32;
+    const int j = lane & (G - 1), half = warp - 2;
+    const int t0 = half * (C::TN / 2) + lane / G;
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int k0 = kb0; k0 < kb1; k0 += G) {
+      const int kb = min(k0 + j, kb1 - 1);  // past the end: any value, it is not used
+      float v[PER_LANE];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    part[warp][8 * n + 2 * q][g] = acc[n][0];
-    part[warp][8 * n + 2 * q + 1][g] = acc[n][1];
-    part[warp][8 * n + 2 * q][g + 8] = acc[n][2];
-    part[warp][8 * n + 2 * q + 1][g + 8] = acc[n][3];
+      for (int i = 0; i < PER_LANE; ++i)
+        v[i] = __ldg(p.s_x + static_cast<size_t>(min(t0 + i * (32 / G), p.T - 1)) * p.kblocks + kb);
+      const int nb = min(o_cta / kFp8Block + half, (p.N - 1) / kFp8Block);
+      const float w = __ldg(p.s_w + static_cast<size_t>(nb) * p.kblocks + kb);
+      if (!wait_all(&sempty_bar[slot], phase ^ 1, abort_flag, p.status, 56)) break;
+      float* g = reinterpret_cast<float*>(smem + p.off_slots) + slot * C::SLOT;
+#pragma unroll
+      for (int i = 0; i < PER_LANE; ++i) g[j * C::SX_ROW + t0 + i * (32 / G)] = v[i];
+      if (lane < G) g[G * C::SX_ROW + half * G + j] = w;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfull_bar[slot]);
+      slot ^= 1;
+      phase ^= slot == 0;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------ accumulation
+    // Two warps per TMEM lane quadrant, each with half of the columns.
+    const int quad = warp & 3, part = (warp - 4) >> 2;
+    const int row = quad * 32 + lane;
+    const int col0 = part * COLS;
+    const int wb = (o_cta + row) / kFp8Block - o_cta / kFp8Block;
+    const uint32_t t_row =
+        tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(part * COLS);
+    uint64_t acc[COLS / 2];
+#pragma unroll
+    for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
+    int buf = 0, slot = 0;
+    uint32_t tphase = 0, sphase = 0;
+    bool ok = true;
+    const float* g = nullptr;
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1; kb += C::BATCH) {
+      const int j = (kb - kb0) & (G - 1);  // G is a multiple of BATCH
+      if (j == 0) {
+        g = reinterpret_cast<const float*>(smem + p.off_slots) + slot * C::SLOT;
+        ok = wait_all(&sfull_bar[slot], sphase, abort_flag, p.status, 57);
+      }
+      ok = ok && wait_all(&tfull_bar[buf], tphase, abort_flag, p.status, 58);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = t_row + static_cast<uint32_t>(buf * C::BUF_COLS);
+#pragma unroll
+      for (int c = 0; c < COLS; c += CHUNK) {
+        uint32_t r[C::BATCH][CHUNK];
+#pragma unroll
+        for (int b = 0; b < C::BATCH; ++b)
+          tmem_ld_32x32b(d + static_cast<uint32_t>(b * C::TN + c), r[b]);
+#pragma unroll
+        for (int b = 0; b < C::BATCH; ++b) tmem_ld_wait_for(r[b]);
+        if (c + CHUNK == COLS) {  // the buffer has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+        }
+#pragma unroll
+        for (int b = 0; b < C::BATCH; ++b) {
+          if (kb + b >= kb1) break;  // (the columns of blocks past the end hold anything)
+          // rows past R: any of the slot's numbers
+          const float w = g[G * C::SX_ROW + min(wb, C::W_BLOCKS - 1) * G + j + b];
+          const uint64_t w2 = pack_f32x2(w, w);
+          const float4* sx = reinterpret_cast<const float4*>(g + (j + b) * C::SX_ROW + col0 + c);
+#pragma unroll
+          for (int i = 0; i < CHUNK / 4; ++i) {
+            const float4 x = sx[i];
+            fma_f32x2(acc[c / 2 + 2 * i], r[b][4 * i], r[b][4 * i + 1],
+                      mul_f32x2(pack_f32x2(x.x, x.y), w2));
+            fma_f32x2(acc[c / 2 + 2 * i + 1], r[b][4 * i + 2], r[b][4 * i + 3],
+                      mul_f32x2(pack_f32x2(x.z, x.w), w2));
+          }
+        }
+      }
+      if (++buf == NBUF) {
+        buf = 0;
+        tphase ^= 1;
+      }
+      if (j + C::BATCH == G) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty_bar[slot]);
+        slot ^= 1;
+        sphase ^= slot == 0;
+      }
+    }
+    const int o = o_cta + row;
+    const bool mine = row < p.rows && o < p.N;
+    const float bias =
+        mine && p.bias ? static_cast<float>(static_cast<const E*>(p.bias)[o]) : 0.0f;
+    E* y = static_cast<E*>(p.Y) + o;
+    if (S == 1) {
+      if (ok && mine) {
+#pragma unroll
+        for (int c = 0; c < COLS; c += 2) {
+          const float2 v = unpack_f32x2(acc[c / 2]);
+          const int t = col0 + c;
+          if (t < p.T) y[static_cast<size_t>(t) * p.N] = static_cast<E>(v.x + bias);
+          if (t + 1 < p.T) y[static_cast<size_t>(t + 1) * p.N] = static_cast<E>(v.y + bias);
+        }
+      }
+    } else {
+      // to the token's owner, [source][token / S][row]
+      const int slots = (C::TN + S - 1) / S;
+      const uint32_t xchg = smem_u32(smem + p.off_xchg);
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+          const float2 v = unpack_f32x2(acc[c / 2]);
+          const int t = col0 + c;
+          if (t < p.T)
+            st_cluster_f32(mapa_shared(xchg + (((rank * slots + t / S) * 128 + row) << 2), t % S),
+                           c & 1 ? v.y : v.x);
+        }
+      }
+      __syncwarp();
+      cluster_sync_all();  // all sums have arrived (the other warps: below)
+      const float* in = reinterpret_cast<const float*>(smem + p.off_xchg);
+      if (ok && mine) {
+        // the two warps of a row take turns
+        for (int i = part, t = rank + part * S; t < p.T; i += 2, t += 2 * S) {
+          float v = 0.0f;
+          for (int src = 0; src < S; ++src) v += in[(src * slots + i) * 128 + row];
+          y[static_cast<size_t>(t) * p.N] = static_cast<E>(v + bias);
+        }
+      }
+    }
   }
+  if (S > 1 && warp < 4) {
+    __syncwarp();
+    cluster_sync_all();
+  }
+  tc_fence_before();
   __syncthreads();
-  for (int i = threadIdx.x; i < 8 * NT * kStreamRows; i += 32 * kStreamWarps) {
-    const int c = i / kStreamRows, r = i % kStreamRows;
-    const int t = t0 + c, o = o0 + r;
-    if (t >= p.T || o >= p.N) continue;
-    float v = part[0][c][r];
-#pragma unroll
-    for (int w = 1; w < kStreamWarps; ++w) v += part[w][c][r];
-    if (p.bias) v += static_cast<float>(static_cast<const E*>(p.bias)[o]);
-    static_cast<E*>(p.Y)[static_cast<size_t>(t) * p.N + o] = static_cast<E>(v);
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
+}
+
+template <typename E, class C>
+cudaError_t launch_rows_gemm(const Fp8Params& p, int rows, int split, cudaStream_t st) {
+  auto* kernel = fp8_rows_gemm_kernel<E, C>;
+  static std::atomic<uint64_t> ready{0};
+  int* status = device_status_ptr();
+  if (!status) return cudaErrorUnknown;
+  cudaError_t e = allow_smem(kernel, kRowsSmem, ready);
+  if (e != cudaSuccess) return e;
+  RowsParams rp{};
+  rp.s_x = p.s_x;
+  rp.s_w = p.s_w;
+  rp.bias = p.bias;
+  rp.Y = p.Y;
+  rp.status = status;
+  rp.T = p.T;
+  rp.N = p.N;
+  rp.kblocks = p.kblocks;
+  rp.rows = rows;
+  rp.stage_bytes = (rows + C::TN) * kFp8Block;
+  // the MMAs read whole 128-row tiles, up to `over` bytes past the last stage
+  const int over = std::max(0, (128 - rows - C::TN) * kFp8Block);
+  const int slots = 2 * C::SLOT * 4;
+  const int xchg = split > 1 ? split * ((C::TN + split - 1) / split) * 128 * 4 : 0;
+  const int room = kRowsSmem - 1024 - over - slots - xchg - 16;
+  rp.stages = std::min(std::min(kRowsMaxStages, room / rp.stage_bytes),
+                       (p.kblocks + split - 1) / split);
+  rp.off_slots = (rp.stages * rp.stage_bytes + over + 15) / 16 * 16;
+  rp.off_xchg = rp.off_slots + (slots + 15) / 16 * 16;
+  const int smem = rp.off_xchg + xchg + 1024;
+  CUtensorMap mx, mw;
+  if (!encode_tma_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.Xq, p.K, p.T, p.K, kFp8Block, C::TN,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tma_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.Wq, p.K, p.N, p.K, kFp8Block, rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int grid = ((p.N - 1) / rows + 1) * split;
+  return launch_pdl_cluster(kernel, dim3(grid), dim3(kRowsThreads), smem, st, split, mx, mw, rp);
 }
 
 template <typename E>
-cudaError_t launch_stream(const Fp8Params& p, cudaStream_t st) {
-  auto go = [&](auto* kernel, int nt) {
-    const dim3 grid((p.N + kStreamRows - 1) / kStreamRows, (p.T + 8 * nt - 1) / (8 * nt));
-    return launch_pdl(kernel, grid, dim3(32 * kStreamWarps), 0, st, p);
+cudaError_t launch_rows_any(const Fp8Params& p, cudaStream_t st) {
+  const long long sms = num_sms();
+  const int forced = option(ZQ_OPT_SPLIT_K), cap = option(ZQ_OPT_MAX_CTAS);
+  auto rows_for = [&](long long ctas) {
+    return static_cast<int>(std::min<long long>(128, (p.N + ctas * 8 - 1) / (ctas * 8) * 8));
   };
-  if (p.T <= 8) return go(fp8_stream_kernel<E, 1>, 1);
-  if (p.T <= 16) return go(fp8_stream_kernel<E, 2>, 2);
-  return go(fp8_stream_kernel<E, 4>, 4);
+  // Two CTAs per SM stream large matrices best, one CTA small ones; K is
+  // split until a CTA has 64 rows (8 KB to copy per block) or little of K.
+  // Measured at T = 16 (us): 24576 x 6144 with 280 CTAs of 88 rows 24.7, 147
+  // of 168 rows 26.9; 6144 x 24576 split in four, 280 CTAs, 26.2, in two, 140
+  // CTAs, 32.5, unsplit 55; 2120 x 5008 at T = 32 split in eight, 144 CTAs,
+  // 8.1, 272 CTAs 14.4, unsplit 16.2.
+  const bool large = static_cast<long long>(p.N) * p.K >= (24ll << 20) || p.N > 128 * sms;
+  const long long target = cap ? cap : (large ? 2 * sms : sms);
+  int split = 1;
+  while (split < 8 && rows_for(target / split) < 64 && p.kblocks >= 4 * split) split *= 2;
+  if (forced) split = forced;
+  const int rows = rows_for(std::max<long long>(1, target / split));
+  auto go = [&](auto tn) {
+    return launch_rows_gemm<E, RowsCfg<decltype(tn)::value>>(p, rows, split, st);
+  };
+  if (p.T <= 16) return go(std::integral_constant<int, 16>{});
+  if (p.T <= 32) return go(std::integral_constant<int, 32>{});
+  return go(std::integral_constant<int, 64>{});
 }
 
 // ------------------------------------------------------------------ tiles
@@ -237,35 +557,6 @@ __device__ __forceinline__ void tile_of(int u, const TileParams& p, int& m, int&
   const int gm = min(p.group_m, p.m_tiles - g * p.group_m);
   n = r / gm;
   m = g * p.group_m + r - n * gm;
-}
-
-// Every lane waits (bounded); true when all of them saw the phase complete.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                         int* status, int site) {
-  const bool ok = mbar_wait(bar, parity, abort, status, site);
-  return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
-  asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tfma.rn.f32x2 %0, d, %3, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(lo), "r"(hi), "l"(s));
-}
-
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
 }
 
 // Eight columns' bias, in 16-bit form, added to their sums.
@@ -719,15 +1010,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 template <typename E, class C>
 cudaError_t launch_tile(const Fp8Params& p, int split, int* status, cudaStream_t st) {
   auto* kernel = fp8_tile_kernel<E, C>;
-  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(kernel, C::SMEM_BYTES, ready);
   if (e != cudaSuccess) return e;
-  if (dev > 63 || !(ready.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    if (dev <= 63) ready.fetch_or(1ull << dev);
-  }
   CUtensorMap mx, mw;
   if (!encode_tma_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.Xq, p.K, p.T, p.K, BK, BM,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -787,8 +1072,7 @@ cudaError_t launch_tiles(const Fp8Params& p, cudaStream_t st) {
   while (split < 8 && small * split * 2 <= sms && p.kblocks >= split * 2 * 4) split *= 2;
   if (fsplit) split = fsplit;
   if (split > 1 && !fpair && !fbn) {
-    if (split != 2 && split != 4 && split != 8) return cudaErrorInvalidValue;
-    if (p.kblocks < split) return cudaErrorInvalidValue;
+    while (split & (split - 1)) --split;  // the tiles' columns are shared out evenly
     return launch_tile<E, TileCfg<128, false, true>>(p, split, status, st);
   }
   // cost of a tiling: waves x columns per CTA
@@ -814,7 +1098,10 @@ extern "C" zq_status zq_gemm_fp8(const void* Xq, const float* s_x, const void* W
   if (dtype != ZQ_F16 && dtype != ZQ_BF16) return ZQ_ERR_UNSUPPORTED;
   if (T < 0 || N < 8 || N % 8 != 0 || K < 16 || K > (1 << 20) || K % 16 != 0) return ZQ_ERR_SHAPE;
   const int path = option(ZQ_OPT_GEMM_PATH);
-  if (path > 2) return ZQ_ERR_UNSUPPORTED;
+  const int split = option(ZQ_OPT_SPLIT_K), bn = option(ZQ_OPT_GEMM_BN);
+  if (path > 2 || (path == 2 && T > kRowsMaxTokens) || split > 8 ||
+      split > (K + kFp8Block - 1) / kFp8Block || (bn && bn != 128 && bn != 256))
+    return ZQ_ERR_UNSUPPORTED;
   if (T == 0) return ZQ_OK;
   if (!Xq || !s_x || !Wq || !s_w || !Y) return ZQ_ERR_NULL;
   if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || (bias && !aligned16(bias)) ||
@@ -832,10 +1119,10 @@ extern "C" zq_status zq_gemm_fp8(const void* Xq, const float* s_x, const void* W
   p.K = K;
   p.kblocks = (K + kFp8Block - 1) / kFp8Block;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool tiles = path == 1 || (path == 0 && T > kStreamMaxTokens);
+  const bool rows = path == 2 || (path == 0 && T <= kRowsMaxTokens);
   const cudaError_t e = with_dtype(dtype, [&](auto tag) {
     using E = decltype(tag);
-    return tiles ? launch_tiles<E>(p, st) : launch_stream<E>(p, st);
+    return rows ? launch_rows_any<E>(p, st) : launch_tiles<E>(p, st);
   });
   return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
 }
