@@ -16,76 +16,93 @@
 namespace zq {
 namespace {
 
-constexpr int kVec = 8;                           // values per 16-byte load
-constexpr int kVecsPerBlock = kFp8Block / kVec;   // 16: a half warp holds one block
+// Four lanes hold a block of 128 values: 16-byte vectors l, l + 4, l + 8 and
+// l + 12 of the block in lane l (64 consecutive bytes per load of the four).
+// With 32 values per lane the block's maximum costs two shuffles, and its two
+// divisions are spread over 32 values; with one vector per lane they were
+// half of all instructions (20.4 us for 4096 x 6144 instead of the copy's 12).
+constexpr int kLanes = 4;
+constexpr int kVecs = kFp8Block / 8 / kLanes;  // vectors per lane
+constexpr int kWarpBlocks = 32 / kLanes;       // blocks per warp
 
-// Maximum over the 16 lanes of a half warp (NaN if any lane has it).
-__device__ __forceinline__ float half_warp_max(float v) {
+__device__ __forceinline__ float quad_max(float v) {
+  v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return max_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+// Quantizes a lane's part of a block.  `col` is the block's first column, q
+// and y16 (may be null) its first value's place in the outputs.
+template <typename E>
+__device__ __forceinline__ void finish_block(const uint64_t (&y)[4 * kVecs], int lane, int col,
+                                             int K, uint8_t* q, E* y16, float* s_out) {
+  const BlockScale s = block_scale(quad_max(amax_pairs(y, 0.0f)));
+  if (lane == 0 && col < K) *s_out = s.scale;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  for (int i = 0; i < kVecs; ++i) {
+    const int at = 8 * (lane + kLanes * i);
+    if (col + at < K) {
+      *reinterpret_cast<uint2*>(q + at) = encode8(y + 4 * i, s);
+      if (y16) *reinterpret_cast<uint4*>(y16 + at) = narrow8<E>(y + 4 * i);
+    }
+  }
 }
 
 // ------------------------------------------------- rows without a LayerNorm
 
-// One half warp per block of 128 values, UNROLL blocks with their loads in
-// flight before the first is reduced.  Blocks are numbered row by row, so
-// neighbouring half warps read neighbouring 256-byte pieces.  The last block
-// of a row is short when K is no multiple of 128: its missing lanes hold 0.
-template <typename E, int ACT, int UNROLL>
-__global__ void __launch_bounds__(256)
+constexpr int kRowsCtas = 4;  // CTAs per SM: 64 registers per thread
+
+// Blocks are numbered row by row, so neighbouring lanes read neighbouring
+// pieces.  The last block of a row is short when K is no multiple of 128: its
+// missing lanes hold 0.
+template <typename E, int ACT>
+__global__ void __launch_bounds__(256, kRowsCtas)
     fp8_rows_kernel(const E* __restrict__ X, const E* __restrict__ bias, int K, unsigned kblocks,
                     unsigned long long items, uint8_t* __restrict__ Xq, float* __restrict__ s_blk,
                     E* __restrict__ Y) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & (kVecsPerBlock - 1);
-  const unsigned long long first =
-      blockIdx.x * 16ull * UNROLL + threadIdx.x / kVecsPerBlock;  // 16 half warps per CTA
-  uint4 v[UNROLL];
-  size_t at[UNROLL];
-  int col[UNROLL];
-#pragma unroll
-  for (int u = 0; u < UNROLL; ++u) {
-    const unsigned long long item = first + 16ull * u;
-    unsigned long long row;
-    unsigned blk;
-    if (items <= 0xFFFFFFFFull) {  // 32-bit division whenever the numbers allow it
-      const unsigned r = static_cast<unsigned>(item) / kblocks;
-      row = r;
-      blk = static_cast<unsigned>(item) - r * kblocks;
-    } else {
-      row = item / kblocks;
-      blk = static_cast<unsigned>(item - row * kblocks);
-    }
-    col[u] = static_cast<int>(blk) * kFp8Block + lane * kVec;
-    if (item >= items || col[u] >= K) col[u] = -1;
-    at[u] = static_cast<size_t>(row) * K + (col[u] < 0 ? 0 : col[u]);
-    v[u] = col[u] < 0 ? make_uint4(0, 0, 0, 0)
-                      : __ldcs(reinterpret_cast<const uint4*>(X + at[u]));
+  const int lane = threadIdx.x & (kLanes - 1);
+  const unsigned long long item =
+      static_cast<unsigned long long>(blockIdx.x) * (blockDim.x / kLanes) + threadIdx.x / kLanes;
+  unsigned long long row;
+  unsigned blk;
+  if (items <= 0xFFFFFFFFull) {  // 32-bit division whenever the numbers allow it
+    const unsigned r = static_cast<unsigned>(item) / kblocks;
+    row = r;
+    blk = static_cast<unsigned>(item) - r * kblocks;
+  } else {
+    row = item / kblocks;
+    blk = static_cast<unsigned>(item - row * kblocks);
   }
+  // lanes past the last block take part in the shuffles with nothing to read
+  const int col = item < items ? static_cast<int>(blk) * kFp8Block : K;
+  const size_t at = static_cast<size_t>(row) * K + col;
+  uint4 v[kVecs], b[kVecs];
 #pragma unroll
-  for (int u = 0; u < UNROLL; ++u) {
-    const unsigned long long item = first + 16ull * u;
-    float y[8];
-    unpack8<E>(v[u], y);
-    if (bias && col[u] >= 0) {
-      float b[8];
-      unpack8<E>(__ldg(reinterpret_cast<const uint4*>(bias + col[u])), b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __fadd_rn(y[i], b[i]);
-    }
-    if (ACT == ZQ_ACT_GELU) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = gelu_erf(y[i]);
-    }
-    const BlockScale s = block_scale(half_warp_max(amax8(y)));
-    if (item < items && lane == 0) s_blk[item] = s.scale;
-    if (col[u] >= 0) {
-      *reinterpret_cast<uint2*>(Xq + at[u]) = encode8(y, s);
-      if (Y) *reinterpret_cast<uint4*>(Y + at[u]) = pack8<E>(y);
+  for (int i = 0; i < kVecs; ++i) {
+    const int o = 8 * (lane + kLanes * i);
+    v[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (col + o < K) {
+      v[i] = __ldcs(reinterpret_cast<const uint4*>(X + at + o));
+      if (bias) b[i] = __ldg(reinterpret_cast<const uint4*>(bias + col + o));
     }
   }
+  uint64_t y[4 * kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, c[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint64_t p = widen2<E>(w[j]);
+      if (bias) p = add_f32x2(p, widen2<E>(c[j]));
+      if (ACT == ZQ_ACT_GELU) {
+        const float2 f = unpack_f32x2(p), e = gelu_pair(f.x, f.y);
+        p = pack_f32x2(e.x, e.y);
+      }
+      y[4 * i + j] = p;
+    }
+  }
+  finish_block<E>(y, lane, col, K, Xq + at, Y ? Y + at : nullptr, s_blk + item);
 }
 
 template <typename E, int ACT>
@@ -93,15 +110,14 @@ cudaError_t launch_rows(const void* X, const void* bias, int T, int K, void* Xq,
                         void* Y, cudaStream_t st) {
   const unsigned kblocks = (K + kFp8Block - 1) / kFp8Block;
   const unsigned long long items = static_cast<unsigned long long>(T) * kblocks;
-  auto go = [&](auto* kernel, int unroll) {
-    const unsigned long long per_cta = 16ull * unroll;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>((items + per_cta - 1) / per_cta)),
-                      dim3(256), 0, st, static_cast<const E*>(X), static_cast<const E*>(bias), K,
-                      kblocks, items, static_cast<uint8_t*>(Xq), s_blk, static_cast<E*>(Y));
-  };
-  // one block per half warp while that leaves SMs without work
-  if (items <= 16ull * 4 * 4 * num_sms()) return go(fp8_rows_kernel<E, ACT, 1>, 1);
-  return go(fp8_rows_kernel<E, ACT, 4>, 4);
+  // small CTAs while there are too few blocks to give every SM a large one
+  const unsigned threads = items * kLanes <= 256ull * num_sms() ? 64 : 256;
+  const unsigned long long per_cta = threads / kLanes;
+  const unsigned long long ctas = (items + per_cta - 1) / per_cta;
+  if (ctas > 0x7fffffffull) return cudaErrorInvalidValue;
+  return launch_pdl(fp8_rows_kernel<E, ACT>, dim3(static_cast<unsigned>(ctas)), dim3(threads), 0,
+                    st, static_cast<const E*>(X), static_cast<const E*>(bias), K, kblocks, items,
+                    static_cast<uint8_t*>(Xq), s_blk, static_cast<E*>(Y));
 }
 
 // ------------------------------------------------------ rows after a LayerNorm
@@ -112,143 +128,123 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the W warps of a row; every thread gets it.  `red` is used once
-// per barrier interval.
-template <int W>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+// Sum over the `warps` warps of a row (the CTA); every thread gets it.  `red`
+// is written once between two uses of the other buffers.
+__device__ __forceinline__ float row_sum(float v, float* red, int warps) {
   v = warp_sum(v);
-  if (W == 1) return v;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if (warps == 1) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int w = 0; w < W; ++w) s += red[w];
-  return s;
+  return warp_sum(lane < warps ? red[lane] : 0.0f);
 }
 
-// W warps per row (one row at a time per CTA; with W = 1 a CTA of four warps
-// has four rows), VPT 16-byte vectors per thread: the row is read once, its
-// mean and then its centred sum of squares are taken over the registers in
-// fp32, and each half warp quantizes the blocks that it holds.  The CTAs stay
-// for many rows: gamma and beta are kept in registers, and the next row's
-// loads are issued before the current one is reduced.
-template <typename E, int W, int VPT>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
+// A warp has 1024 consecutive values of a row, 32 per lane; the row is read
+// once, its mean and then its centred sum of squares are taken over the
+// registers in fp32.  Rows of up to 1024 values: one per warp (ROWS = 4 to a
+// CTA), longer ones: one per CTA of at most THREADS.  The CTAs stay for many
+// rows; up to 512 threads the next row's loads are issued before the current
+// row is reduced (80 registers; with 64, for 32 warps per SM, they spill:
+// 29.0 instead of 21.7 us for 4096 x 6144, and 22.9 without them).  gamma and
+// beta come from L1.
+template <typename E, int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS < 1024 ? 768 / THREADS : 1)
     fp8_ln_kernel(const E* __restrict__ X, const E* __restrict__ gamma, const E* __restrict__ beta,
                   int T, int K, float eps, uint8_t* __restrict__ Xq, float* __restrict__ s_blk,
                   E* __restrict__ Y) {
-  constexpr int ROWS = W == 1 ? 4 : 1;
-  constexpr int RT = 32 * W;  // threads of a row
-  __shared__ float red[2][2][W];
+  __shared__ float red[2][2][32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int tid = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
-  const int kvecs = K / kVec, kblocks = (K + kFp8Block - 1) / kFp8Block;
+  const int warps = ROWS > 1 ? 1 : blockDim.x / 32;
+  const int tid = ROWS > 1 ? (threadIdx.x & 31) : threadIdx.x;
+  const int lane = tid & (kLanes - 1), blk = tid / kLanes, col = blk * kFp8Block;
+  const int kblocks = (K + kFp8Block - 1) / kFp8Block;
   const float inv_k = __fdiv_rn(1.0f, static_cast<float>(K));
-  uint4 g[VPT], b[VPT], x[VPT];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto offset = [&](int i) { return col + 8 * (lane + kLanes * i); };
+  const long long stride = static_cast<long long>(gridDim.x) * ROWS;
+  long long row = static_cast<long long>(blockIdx.x) * ROWS + (ROWS > 1 ? threadIdx.x / 32 : 0);
+  uint4 x[kVecs];
+  auto fetch = [&](long long r) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = i * RT + tid;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    g[i] = v < kvecs ? __ldg(reinterpret_cast<const uint4*>(gamma) + v) : zero;
-    b[i] = v < kvecs && beta ? __ldg(reinterpret_cast<const uint4*>(beta) + v) : zero;
-    x[i] = zero;
-  }
-  const int stride = gridDim.x * ROWS;
-  int row = blockIdx.x * ROWS + (W == 1 ? threadIdx.x >> 5 : 0);
-  auto fetch = [&](int r) {
-    if (r >= T) return;
-    const uint4* src = reinterpret_cast<const uint4*>(X + static_cast<size_t>(r) * K);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (i * RT + tid < kvecs) x[i] = __ldcs(src + i * RT + tid);
+    for (int i = 0; i < kVecs; ++i)
+      x[i] = r < T && offset(i) < K
+                 ? __ldcs(reinterpret_cast<const uint4*>(X + r * K + offset(i)))
+                 : zero;
   };
-  fetch(row);
-  for (int turn = 0; row < T; turn ^= 1) {
-    float y[VPT][8];
-    float sum = 0.0f;
+  constexpr bool kAhead = THREADS < 1024;
+  if (kAhead) fetch(row);
+  for (int turn = 0; row < T; row += stride, turn ^= 1) {
+    if (!kAhead) fetch(row);
+    uint64_t y[4 * kVecs];
+    uint64_t sum2 = 0ull;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      unpack8<E>(x[i], y[i]);
-      sum += ((y[i][0] + y[i][1]) + (y[i][2] + y[i][3])) +
-             ((y[i][4] + y[i][5]) + (y[i][6] + y[i][7]));
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[4 * i + j] = widen2<E>(w[j]);
+        sum2 = add_f32x2(sum2, y[4 * i + j]);
+      }
     }
-    const int next = static_cast<int>(min(static_cast<long long>(row) + stride, 0x7fffffffll));
-    fetch(next);
-    const float mean = row_sum<W>(sum, red[turn][0]) * inv_k;
-    float sq = 0.0f;
+    if (kAhead) fetch(row + stride);
+    const float2 s2 = unpack_f32x2(sum2);
+    const float mean = row_sum(s2.x + s2.y, red[turn][0], warps) * inv_k;
+    const uint64_t minus = pack_f32x2(-mean, -mean);
+    uint64_t sq2 = 0ull;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if (i * RT + tid < kvecs) {
+    for (int i = 0; i < kVecs; ++i) {
+      if (offset(i) < K) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[i][e] -= mean;
-          sq = fmaf(y[i][e], y[i][e], sq);
+        for (int j = 4 * i; j < 4 * i + 4; ++j) {
+          y[j] = add_f32x2(y[j], minus);
+          sq2 = fma_f32x2(y[j], y[j], sq2);
         }
       }
     }
-    const float var = row_sum<W>(sq, red[turn][1]) * inv_k;
+    const float2 q2 = unpack_f32x2(sq2);
+    const float var = row_sum(q2.x + q2.y, red[turn][1], warps) * inv_k;
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + eps));
-    uint8_t* qrow = Xq + static_cast<size_t>(row) * K;
+    const uint64_t rstd2 = pack_f32x2(rstd, rstd);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * RT + tid;
-      float gf[8], bf[8];
-      unpack8<E>(g[i], gf);
-      unpack8<E>(b[i], bf);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[i][e] = fmaf(y[i][e] * rstd, gf[e], bf[e]);  // 0 past K
-      const BlockScale s = block_scale(half_warp_max(amax8(y[i])));
-      if (v < kvecs) {
-        reinterpret_cast<uint2*>(qrow)[v] = encode8(y[i], s);
-        if (Y) reinterpret_cast<uint4*>(Y + static_cast<size_t>(row) * K)[v] = pack8<E>(y[i]);
-        if ((v & (kVecsPerBlock - 1)) == 0)
-          s_blk[static_cast<size_t>(row) * kblocks + v / kVecsPerBlock] = s.scale;
+    for (int i = 0; i < kVecs; ++i) {
+      uint4 g = zero, b = zero;  // 0 past K
+      if (offset(i) < K) {
+        g = __ldg(reinterpret_cast<const uint4*>(gamma + offset(i)));
+        if (beta) b = __ldg(reinterpret_cast<const uint4*>(beta + offset(i)));
       }
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        y[4 * i + j] = fma_f32x2(mul_f32x2(y[4 * i + j], rstd2), widen2<E>(gw[j]), widen2<E>(bw[j]));
     }
-    row = next;
+    const size_t at = static_cast<size_t>(row) * K + col;
+    finish_block<E>(y, lane, col, K, Xq + at, Y ? Y + at : nullptr,
+                    s_blk + static_cast<size_t>(row) * kblocks + blk);
   }
 }
 
-template <typename E, int W, int VPT>
-cudaError_t launch_ln_one(const void* X, const void* gamma, const void* beta, int T, int K,
-                          float eps, void* Xq, float* s_blk, void* Y, cudaStream_t st) {
-  constexpr int ROWS = W == 1 ? 4 : 1;
-  constexpr int THREADS = W == 1 ? 128 : 32 * W;
+template <typename E, int ROWS, int THREADS>
+cudaError_t launch_ln_one(int threads, const void* X, const void* gamma, const void* beta, int T,
+                          int K, float eps, void* Xq, float* s_blk, void* Y, cudaStream_t st) {
   const int ctas = (T - 1) / ROWS + 1;
-  const int resident = num_sms() * std::max(1, 1024 / THREADS);
-  return launch_pdl(fp8_ln_kernel<E, W, VPT>, dim3(std::min(ctas, resident)), dim3(THREADS), 0, st,
-                    static_cast<const E*>(X), static_cast<const E*>(gamma),
+  const int per_sm = 65536 / ((THREADS < 1024 ? 80 : 64) * threads);  // by their registers
+  return launch_pdl(fp8_ln_kernel<E, ROWS, THREADS>, dim3(std::min(ctas, num_sms() * per_sm)),
+                    dim3(threads), 0, st, static_cast<const E*>(X), static_cast<const E*>(gamma),
                     static_cast<const E*>(beta), T, K, eps, static_cast<uint8_t*>(Xq), s_blk,
                     static_cast<E*>(Y));
-}
-
-template <typename E, int W>
-cudaError_t launch_ln_w(int vpt, const void* X, const void* gamma, const void* beta, int T, int K,
-                        float eps, void* Xq, float* s_blk, void* Y, cudaStream_t st) {
-  switch (vpt) {
-    case 1: return launch_ln_one<E, W, 1>(X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-    case 2: return launch_ln_one<E, W, 2>(X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-    case 3: return launch_ln_one<E, W, 3>(X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-    default: return launch_ln_one<E, W, 4>(X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-  }
 }
 
 template <typename E>
 cudaError_t launch_ln(const void* X, const void* gamma, const void* beta, int T, int K, float eps,
                       void* Xq, float* s_blk, void* Y, cudaStream_t st) {
-  const int warps1 = (K / kVec + 31) / 32;  // warps of a row with one vector per thread
-  int W = 1;
-  while (W * 4 < warps1) W *= 2;
-  const int vpt = (warps1 + W - 1) / W;
-  switch (W) {
-    case 1: return launch_ln_w<E, 1>(vpt, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-    case 2: return launch_ln_w<E, 2>(vpt, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-    case 4: return launch_ln_w<E, 4>(vpt, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-    case 8: return launch_ln_w<E, 8>(vpt, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-    case 16: return launch_ln_w<E, 16>(vpt, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-    default: return launch_ln_w<E, 32>(vpt, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-  }
+  const int warps = (K + 1023) / 1024;
+  if (warps == 1) return launch_ln_one<E, 4, 128>(128, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
+  if (warps <= 8)
+    return launch_ln_one<E, 1, 256>(32 * warps, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
+  if (warps <= 16)
+    return launch_ln_one<E, 1, 512>(32 * warps, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
+  return launch_ln_one<E, 1, 1024>(32 * warps, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
 }
 
 // -------------------------------------------------------------------- weights
@@ -263,7 +259,7 @@ __global__ void __launch_bounds__(256)
   grid_dependency_wait();
   grid_launch_dependents();
   const unsigned nb = blockIdx.x / kblocks, kb = blockIdx.x - nb * kblocks;
-  const int col = static_cast<int>(kb) * kFp8Block + (threadIdx.x & 15) * kVec;
+  const int col = static_cast<int>(kb) * kFp8Block + (threadIdx.x & 15) * 8;
   const int row0 = static_cast<int>(nb) * kFp8Block + (threadIdx.x >> 4);
   uint4 v[8];
 #pragma unroll
@@ -276,9 +272,9 @@ __global__ void __launch_bounds__(256)
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float y[8];
-    unpack8<E>(v[i], y);
-    m = max_nan(m, amax8(y));
+    uint64_t y[4];
+    widen8<E>(v[i], y);
+    m = amax_pairs(y, m);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -292,8 +288,8 @@ __global__ void __launch_bounds__(256)
   for (int i = 0; i < 8; ++i) {
     const int r = row0 + 16 * i;
     if (r < N && col < K) {
-      float y[8];
-      unpack8<E>(v[i], y);
+      uint64_t y[4];
+      widen8<E>(v[i], y);
       *reinterpret_cast<uint2*>(Wq + static_cast<size_t>(r) * K + col) = encode8(y, s);
     }
   }

@@ -60,6 +60,54 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// max(a, |b|, |c|) for a >= 0, NaN if any is.
+__device__ __forceinline__ float max_nan_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two fp32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The two 16-bit values of a word as a pair of fp32.
+template <typename E>
+__device__ __forceinline__ uint64_t widen2(uint32_t w) {
+  const float2 f = unpack2<E>(w);
+  return pack_f32x2(f.x, f.y);
+}
+
+template <typename E>
+__device__ __forceinline__ void widen8(const uint4& v, uint64_t (&y)[4]) {
+  y[0] = widen2<E>(v.x);
+  y[1] = widen2<E>(v.y);
+  y[2] = widen2<E>(v.z);
+  y[3] = widen2<E>(v.w);
+}
+
 // The factors that turn the values of one block into codes.  With
 // a = max(amax, 2^-110), the code of y is the e4m3 value nearest to
 // y * (448 / a).  448 / a is held as hi + lo (lo the remainder of the
@@ -70,41 +118,68 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // An all-zero block has scale 0 and codes 0; one that holds Inf or NaN has
 // scale Inf or NaN and NaN codes.
 struct BlockScale {
-  float hi, lo, scale;
+  uint64_t hi, lo;  // twice each
+  float scale;
 };
 __device__ __forceinline__ BlockScale block_scale(float amax) {
   BlockScale r;
   if (amax == 0.0f) {
-    r.hi = r.lo = r.scale = 0.0f;
+    r.hi = r.lo = 0ull;
+    r.scale = 0.0f;
     return r;
   }
+  // 1 / a from the hardware's approximation and a Newton step; each quotient
+  // is then corrected by its exact remainder (Markstein's method)
   const float a = max_nan(amax, kAmaxFloor);
-  r.hi = __fdiv_rn(kE4m3Max, a);
-  r.lo = __fmaf_rn(-r.hi, a, kE4m3Max) * (r.hi * (1.0f / kE4m3Max));
-  r.scale = __fdiv_rn(a, kE4m3Max);
+  float rcp;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(rcp) : "f"(a));
+  rcp = __fmaf_rn(__fmaf_rn(-a, rcp, 1.0f), rcp, rcp);
+  const float hi = kE4m3Max * rcp;
+  const float lo = __fmaf_rn(-hi, a, kE4m3Max) * rcp;
+  r.hi = pack_f32x2(hi, hi);
+  r.lo = pack_f32x2(lo, lo);
+  constexpr float kInv = 1.0f / kE4m3Max;
+  const float s = a * kInv;
+  r.scale = __fmaf_rn(__fmaf_rn(-kE4m3Max, s, a), kInv, s);
   return r;
 }
 
-// Four codes in one word, the first in the lowest byte (rounded to nearest
-// even; finite values never pass 448, NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+// Two codes, the first in the low byte (rounded to nearest even; finite
+// values never pass 448, NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2(uint64_t v) {
+  const float2 f = unpack_f32x2(v);
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(f.y), "f"(f.x));
+  return c;
 }
-__device__ __forceinline__ uint2 encode8(const float (&y)[8], const BlockScale& s) {
-  float v[8];
+// Eight codes of four pairs.
+__device__ __forceinline__ uint2 encode8(const uint64_t* y, const BlockScale& s) {
+  uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(y[i], s.hi, __fmul_rn(y[i], s.lo));
-  return make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+  for (int i = 0; i < 4; ++i) c[i] = e4m3x2(fma_f32x2(y[i], s.hi, mul_f32x2(y[i], s.lo)));
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// Largest magnitude of eight values (NaN if any is).
-__device__ __forceinline__ float amax8(const float (&y)[8]) {
-  float m = fabsf(y[0]);
+// Four pairs to eight 16-bit values.
+template <typename E>
+__device__ __forceinline__ uint4 narrow8(const uint64_t* y) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_f32x2(y[i]);
+    w[i] = pack2<E>(f.x, f.y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Largest magnitude of N pairs and m (NaN if any is).
+template <int N>
+__device__ __forceinline__ float amax_pairs(const uint64_t (&y)[N], float m) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 f = unpack_f32x2(y[i]);
+    m = max_nan_abs(m, f.x, f.y);
+  }
   return m;
 }
 
