@@ -371,7 +371,7 @@ zq_status zq_gemm_fp8(const void* Xq, const float* s_x, const void* Wq, const fl
  *              of a head, then weight[d] (NULL = 1) and bias[d] (NULL = 0);
  *              in fp32.  Without a norm weight and bias are ignored.
  *   positions  int32 [T]; a token whose position is negative (padding behind
- *              the last sequence) is neither read nor written.
+ *              the last sequence) is not written.
  *   inv_freq   fp32 [R/2] on the device, radians per position
  *              (zq_rope_frequencies).
  *   layout     ZQ_ROPE_HALF pairs values i and i + R/2 (GPT-NeoX),

@@ -11,6 +11,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "zq_fp8.cuh"
 #include "zq_internal.h"
@@ -19,8 +20,11 @@
 namespace zq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a CTA without a norm, and with one
+constexpr int kNormThreads = 64;
 constexpr int kMaxHeadDim = 256;
+constexpr int kMaxTokens = 16;    // of a CTA
+constexpr int kMaxAngles = 1024;  // sines (and cosines) of a CTA, padded
 
 struct Heads {  // one of queries, keys
   const void* in;
@@ -32,232 +36,420 @@ struct Heads {  // one of queries, keys
 };
 
 struct RopeParams {
-  Heads q, k;
+  Heads set[2];  // queries, keys
   const int32_t* positions;
   const float* inv_freq;
   int T, D, R, norm;
-  int units;      // pairs of vectors that make up a head
-  int chunks;     // CTAs per token
-  int per_chunk;  // heads of a CTA
+  int tokens;     // per CTA
+  int columns;    // CTAs per token tile
   int copy_rest;  // values behind R are written too (other output, or a norm)
   float scale, eps;
 };
 
-template <int BYTES>
-struct VecOf;
-template <>
-struct VecOf<16> {
-  using type = uint4;
-};
-template <>
-struct VecOf<8> {
-  using type = uint2;
-};
-template <>
-struct VecOf<4> {
-  using type = uint32_t;
+// Both values of a rotated pair have to meet in one thread.  Halves layout: a
+// unit is VEC values u VEC.. and the VEC values R / 2 behind them, VEC the
+// widest vector that divides R / 2.  Neighbours: a unit is eight values.
+enum Cut { kHalf8, kHalf4, kHalf2, kNeighbours };
+template <int CUT>
+struct CutOf {
+  static constexpr bool HALF = CUT != kNeighbours;
+  static constexpr int VEC = CUT == kHalf4 ? 4 : (CUT == kHalf2 ? 2 : 8);
+  static constexpr int ANGLES = HALF ? VEC : 4;       // of a unit
+  static constexpr int TAIL = CUT == kHalf2 ? 4 : 8;  // widest aligned vector of the rest
+  __host__ __device__ static int rotated_units(int R) { return HALF ? R / 2 / VEC : (R + 7) / 8; }
+  // first value that no unit has
+  __host__ __device__ static int rest(int R) { return HALF ? R : (R + 7) / 8 * 8; }
+  __host__ __device__ static int tail_units(int D, int R) { return (D - rest(R)) / TAIL; }
 };
 
-template <typename E, int VEC>
-__device__ __forceinline__ void load_vec(const E* p, float (&f)[VEC]) {
-  union {
-    typename VecOf<2 * VEC>::type v;
-    uint32_t w[VEC / 2];
-  } u;
-  u.v = *reinterpret_cast<const decltype(u.v)*>(p);
+// Vectors of 2, 4 or 8 16-bit values in up to four words.
+template <int N>
+__device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
+  if constexpr (N == 8) {
+    const uint4 v = *static_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 4) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *static_cast<const uint32_t*>(p);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
+  if constexpr (N == 8)
+    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else if constexpr (N == 4)
+    *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else
+    *static_cast<uint32_t*>(p) = w[0];
+}
+template <typename E, int N>
+__device__ __forceinline__ void widen(const uint32_t* w, float* f) {
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) {
-    const float2 t = unpack2<E>(u.w[i]);
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 t = unpack2<E>(w[i]);
     f[2 * i] = t.x;
     f[2 * i + 1] = t.y;
   }
 }
-template <typename E, int VEC>
-__device__ __forceinline__ void store_vec(E* p, const float (&f)[VEC]) {
-  union {
-    typename VecOf<2 * VEC>::type v;
-    uint32_t w[VEC / 2];
-  } u;
+template <typename E, int N>
+__device__ __forceinline__ void narrow(const float* f, uint32_t* w) {
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) u.w[i] = pack2<E>(f[2 * i], f[2 * i + 1]);
-  *reinterpret_cast<decltype(u.v)*>(p) = u.v;
+  for (int i = 0; i < N / 2; ++i) w[i] = pack2<E>(f[2 * i], f[2 * i + 1]);
+}
+// N floats of shared memory, aligned to their size (16 bytes at most).
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float* f) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+    }
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    f[0] = v.x, f[1] = v.y;
+  }
+}
+// Rotates the pairs (x[i], y[i]), or the neighbours in x.
+template <int N>
+__device__ __forceinline__ void rotate_halves(float* x, float* y, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float v = x[i];
+    x[i] = v * c[i] - y[i] * s[i];
+    y[i] = y[i] * c[i] + v * s[i];
+  }
+}
+__device__ __forceinline__ void rotate_neighbours(float* x, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float v = x[2 * i];
+    x[2 * i] = v * c[i] - x[2 * i + 1] * s[i];
+    x[2 * i + 1] = x[2 * i + 1] * c[i] + v * s[i];
+  }
 }
 
-// A head is cut into units of two vectors of VEC values, so that a lane has
-// both values of every pair it rotates.  Halves layout: unit u < R / 2 / VEC
-// holds values u VEC.. and R / 2 + u VEC..; neighbours layout: 2 u VEC.. and
-// the vector after it.  Units behind the rotated ones hold two neighbouring
-// vectors.  A group of 2^k lanes has a head, NU units to a lane.
-template <typename E, int VEC, int NU, bool HALF, bool NORM>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p, int lanes) {
-  __shared__ float cs[kMaxHeadDim / 2], sn[kMaxHeadDim / 2];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const unsigned token = blockIdx.x / p.chunks;
-  const int chunk = static_cast<int>(blockIdx.x - token * p.chunks);
-  const int pos = __ldg(p.positions + token);
-  if (pos < 0) return;  // a row behind the last sequence: left as it is
+// A CTA has a tile of tokens and one column of threads over the heads: a
+// thread keeps its place in its head and goes through the tile's tokens, so
+// that its addresses move by one addition.  The tile's sines and cosines are
+// computed first, with all threads.
+struct Tile {
+  int column, tokens, row;  // row: angles of a token, padded with (1, 0)
+  long long token0;
+};
+__device__ __forceinline__ Tile tile_of(const RopeParams& p) {
+  const unsigned tile = blockIdx.x / p.columns;
+  Tile t;
+  t.column = static_cast<int>(blockIdx.x - tile * p.columns);
+  t.token0 = static_cast<long long>(tile) * p.tokens;
+  t.tokens = static_cast<int>(min(static_cast<long long>(p.tokens), p.T - t.token0));
+  t.row = (p.R / 2 + 3) & ~3;
+  return t;
+}
+__device__ __forceinline__ void tile_angles(const RopeParams& p, const Tile& t, float* cs, float* sn,
+                                            int* pos) {
+  const int half = p.R / 2;
   // The angle in turns, reduced to half a turn on either side in 64 bits (the
   // product of a position and an fp32 frequency is exact there), so that far
   // positions lose nothing before the fp32 sine and cosine.
-  for (int i = threadIdx.x; i < p.R / 2; i += kThreads) {
-    const double turns = static_cast<double>(pos) * static_cast<double>(__ldg(p.inv_freq + i)) *
-                         0.15915494309189533577;  // 1 / (2 pi)
-    float s, c;
-    sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
-    cs[i] = c * p.scale;
-    sn[i] = s * p.scale;
+  for (int i = threadIdx.x; i < t.tokens * t.row; i += blockDim.x) {
+    const int k = i / t.row, f = i - k * t.row;
+    float s = 0.0f, c = 1.0f;
+    if (f < half) {
+      const double turns = static_cast<double>(__ldg(p.positions + t.token0 + k)) *
+                           static_cast<double>(__ldg(p.inv_freq + f)) *
+                           0.15915494309189533577;  // 1 / (2 pi)
+      sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
+      s *= p.scale;
+      c *= p.scale;
+    }
+    cs[i] = c;
+    sn[i] = s;
   }
+  if (threadIdx.x < t.tokens) pos[threadIdx.x] = __ldg(p.positions + t.token0 + threadIdx.x);
   __syncthreads();
+}
+
+// Without a norm.  Threads of rotated units come first, then (to another
+// output) threads that copy the rest; each has the loads of AHEAD tokens in
+// flight.  A token whose position is negative is passed over.
+template <typename E, int CUT>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  using C = CutOf<CUT>;
+  constexpr int VEC = C::VEC, TAIL = C::TAIL, ANG = C::ANGLES, AHEAD = 4;
+  __shared__ __align__(16) float cs[kMaxAngles], sn[kMaxAngles];
+  __shared__ int pos[kMaxTokens];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const Tile tl = tile_of(p);
+  tile_angles(p, tl, cs, sn, pos);
+  const int heads = p.set[0].n + p.set[1].n, half = p.R / 2;
+  const int ru = C::rotated_units(p.R), tu = p.copy_rest ? C::tail_units(p.D, p.R) : 0;
+  int c = tl.column * kThreads + static_cast<int>(threadIdx.x);
+  const bool rotates = c < heads * ru;
+  if (!rotates) c -= heads * ru;
+  const int per_head = rotates ? ru : tu;
+  if (per_head == 0 || c >= heads * per_head) return;
+  int head = c / per_head;
+  const int u = c - head * per_head;
+  const int which = head >= p.set[0].n;
+  if (which) head -= p.set[0].n;
+  const Heads& hd = p.set[which];
+  const int at = rotates ? u * VEC : C::rest(p.R) + u * TAIL;
+  const E* in = static_cast<const E*>(hd.in) + tl.token0 * hd.in_token + head * hd.in_head + at;
+  E* out = static_cast<E*>(hd.out) + tl.token0 * hd.out_token + head * hd.out_head + at;
+  const long long di = hd.in_token, od = hd.out_token;
+  if (rotates) {
+    for (int t0 = 0; t0 < tl.tokens; t0 += AHEAD) {
+      uint32_t a[AHEAD][VEC / 2], b[AHEAD][VEC / 2];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (t0 + k < tl.tokens) {
+          load_words<VEC>(in + k * di, a[k]);
+          if constexpr (C::HALF) load_words<VEC>(in + k * di + half, b[k]);
+        }
+      in += AHEAD * di;
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        if (t0 + k < tl.tokens && pos[t0 + k] >= 0) {
+          float x[VEC], co[ANG], si[ANG];
+          load_floats<ANG>(cs + (t0 + k) * tl.row + u * ANG, co);
+          load_floats<ANG>(sn + (t0 + k) * tl.row + u * ANG, si);
+          widen<E, VEC>(a[k], x);
+          if constexpr (C::HALF) {
+            float y[VEC];
+            widen<E, VEC>(b[k], y);
+            rotate_halves<VEC>(x, y, co, si);
+            narrow<E, VEC>(y, b[k]);
+            store_words<VEC>(out + half, b[k]);
+          } else {
+            rotate_neighbours(x, co, si);
+          }
+          narrow<E, VEC>(x, a[k]);
+          store_words<VEC>(out, a[k]);
+        }
+        out += od;
+      }
+    }
+  } else {
+    for (int t0 = 0; t0 < tl.tokens; t0 += AHEAD) {
+      uint32_t a[AHEAD][TAIL / 2];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (t0 + k < tl.tokens) load_words<TAIL>(in + k * di, a[k]);
+      in += AHEAD * di;
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        if (t0 + k < tl.tokens && pos[t0 + k] >= 0) store_words<TAIL>(out, a[k]);
+        out += od;
+      }
+    }
+  }
+}
+
+// With a norm: 2^k lanes have a head, NU units to a lane.  Units behind the
+// rotated ones have 2 TAIL neighbouring values of the rest (in the neighbours
+// layout all units are two vectors of eight neighbouring values), so that
+// every lane has two vectors a and b.
+template <int CUT>
+struct NormCut {
+  using C = CutOf<CUT>;
+  static constexpr int VEC = C::VEC, TAIL = VEC == 8 ? 8 : 4, WIDE = TAIL > VEC ? TAIL : VEC;
+  static constexpr int NU = CUT == kHalf2 ? 2 : 1;
+  __host__ __device__ static int rotated(int R) { return C::HALF ? R / 2 / VEC : 0; }
+  __host__ __device__ static int units(int D, int R) {
+    return rotated(R) + ((C::HALF ? D - R : D) + 2 * TAIL - 1) / (2 * TAIL);
+  }
+};
+
+template <typename E, int CUT>
+__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const RopeParams p, int lanes) {
+  using C = NormCut<CUT>;
+  constexpr bool HALF = CutOf<CUT>::HALF;
+  constexpr int NU = C::NU, VEC = C::VEC, TAIL = C::TAIL, WIDE = C::WIDE;
+  __shared__ __align__(16) float cs[kMaxAngles], sn[kMaxAngles];
+  __shared__ int pos[kMaxTokens];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const Tile tl = tile_of(p);
   const int lane = threadIdx.x & (lanes - 1);
-  const int groups = kThreads / lanes;
-  const int half = p.R / 2;
-  const int rot_units = HALF ? half / VEC : (p.R / VEC + 1) / 2;
-  const int h1 = min(p.q.n + p.k.n, (chunk + 1) * p.per_chunk);
-  // all lanes of a warp make the same number of turns: the group reductions need them
-  for (int h0 = chunk * p.per_chunk; h0 < h1; h0 += groups) {
-    const int h = h0 + static_cast<int>(threadIdx.x) / lanes;
-    const bool live = h < h1;
-    const bool is_k = h >= p.q.n;
-    const Heads& hd = is_k ? p.k : p.q;
-    const int hh = live ? (is_k ? h - p.q.n : h) : 0;
-    const E* src = static_cast<const E*>(hd.in) + token * hd.in_token + hh * hd.in_head;
-    E* dst = static_cast<E*>(hd.out) + token * hd.out_token + hh * hd.out_head;
-    float a[NU][VEC], b[NU][VEC];
-    int oa[NU], ob[NU];  // value offsets of the unit's vectors, -1 = none
+  int head = (tl.column * kNormThreads + static_cast<int>(threadIdx.x)) / lanes;
+  // lanes past the last head go along for the group sums, with nothing to read
+  const bool live = head < p.set[0].n + p.set[1].n;
+  const int which = live && head >= p.set[0].n;
+  if (which) head -= p.set[0].n;
+  if (!live) head = 0;
+  const Heads& hd = p.set[which];
+  // value offsets of this lane's vectors (-1 = none), and whether they rotate
+  int oa[NU], ob[NU];
+  bool rot[NU];
+#pragma unroll
+  for (int n = 0; n < NU; ++n) {
+    const int u = lane + n * lanes, ru = C::rotated(p.R);
+    rot[n] = HALF && u < ru;
+    oa[n] = rot[n] ? u * VEC : (HALF ? p.R : 0) + 2 * (u - ru) * TAIL;
+    ob[n] = rot[n] ? p.R / 2 + u * VEC : oa[n] + TAIL;
+    if (!live || oa[n] >= p.D) oa[n] = -1;
+    if (!live || ob[n] >= p.D) ob[n] = -1;
+  }
+  auto load = [&](const E* src, int n, uint32_t* a, uint32_t* b) {
+    if (VEC != TAIL && rot[n]) {
+      if (oa[n] >= 0) load_words<VEC>(src + oa[n], a);
+      if (ob[n] >= 0) load_words<VEC>(src + ob[n], b);
+    } else {
+      if (oa[n] >= 0) load_words<TAIL>(src + oa[n], a);
+      if (ob[n] >= 0) load_words<TAIL>(src + ob[n], b);
+    }
+  };
+  // the norm's weight and bias at this lane's values, for all tokens
+  constexpr uint32_t kOnes = std::is_same<E, __half>::value ? 0x3C003C00u : 0x3F803F80u;
+  uint32_t wa[NU][WIDE / 2], wb[NU][WIDE / 2], ba[NU][WIDE / 2], bb[NU][WIDE / 2];
+#pragma unroll
+  for (int n = 0; n < NU; ++n) {
+#pragma unroll
+    for (int i = 0; i < WIDE / 2; ++i) wa[n][i] = wb[n][i] = kOnes, ba[n][i] = bb[n][i] = 0;
+    if (hd.weight) load(static_cast<const E*>(hd.weight), n, wa[n], wb[n]);
+    if (hd.bias) load(static_cast<const E*>(hd.bias), n, ba[n], bb[n]);
+  }
+  const E* in = static_cast<const E*>(hd.in) + tl.token0 * hd.in_token + head * hd.in_head;
+  E* out = static_cast<E*>(hd.out) + tl.token0 * hd.out_token + head * hd.out_head;
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(p.D));
+  auto group_sum = [&](float v) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  uint32_t ra[NU][WIDE / 2], rb[NU][WIDE / 2];
+  auto fetch = [&] {
 #pragma unroll
     for (int n = 0; n < NU; ++n) {
-      const int u = lane + n * lanes;
-      oa[n] = ob[n] = -1;
-      if (live && u < p.units) {
-        if (HALF && u < rot_units) {
-          oa[n] = u * VEC;
-          ob[n] = half + u * VEC;
-        } else {
-          oa[n] = HALF ? p.R + 2 * (u - rot_units) * VEC : 2 * u * VEC;
-          ob[n] = oa[n] + VEC;
-          if (!p.copy_rest && oa[n] >= p.R) oa[n] = -1;  // nothing to change there
-          if (ob[n] >= p.D || (!p.copy_rest && ob[n] >= p.R)) ob[n] = -1;
-        }
-      }
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) a[n][i] = b[n][i] = 0.0f;
-      if (oa[n] >= 0) load_vec<E, VEC>(src + oa[n], a[n]);
-      if (ob[n] >= 0) load_vec<E, VEC>(src + ob[n], b[n]);
+      for (int i = 0; i < WIDE / 2; ++i) ra[n][i] = rb[n][i] = 0;
+      load(in, n, ra[n], rb[n]);
     }
-    if (NORM) {
-      auto group_sum = [&](float v) {
-        for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-      };
-      const float inv_d = __fdiv_rn(1.0f, static_cast<float>(p.D));
-      if (p.norm == ZQ_NORM_LAYER) {
-        float s = 0.0f;
+    in += hd.in_token;
+  };
+  fetch();  // on its way during the sines
+  tile_angles(p, tl, cs, sn, pos);
+  for (int t = 0; t < tl.tokens; ++t) {
+    float a[NU][WIDE], b[NU][WIDE];
 #pragma unroll
-        for (int n = 0; n < NU; ++n)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) s += a[n][i] + b[n][i];
-        const float mean = group_sum(s) * inv_d;
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            if (oa[n] >= 0) a[n][i] -= mean;
-            if (ob[n] >= 0) b[n][i] -= mean;
-          }
-      }
-      float q = 0.0f;
+    for (int n = 0; n < NU; ++n) {
+      widen<E, WIDE>(ra[n], a[n]);
+      widen<E, WIDE>(rb[n], b[n]);
+    }
+    if (t + 1 < tl.tokens) fetch();  // the next token's, ahead of this one's sums
+    // (vectors that are not there, and the unused end of a short one, are 0)
+    if (p.norm == ZQ_NORM_LAYER) {
+      float sum = 0.0f;
 #pragma unroll
       for (int n = 0; n < NU; ++n)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) q = fmaf(a[n][i], a[n][i], fmaf(b[n][i], b[n][i], q));
-      const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(group_sum(q), inv_d, p.eps)));
-      const E* w = static_cast<const E*>(hd.weight);
-      const E* bs = static_cast<const E*>(hd.bias);
-      auto affine = [&](float (&v)[VEC], int off) {
-        if (off < 0) return;
-        float wv[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) wv[i] = 1.0f;
-        if (w) load_vec<E, VEC>(w + off, wv);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = v[i] * rstd * wv[i];
-        if (bs) {
-          load_vec<E, VEC>(bs + off, wv);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[i] += wv[i];
-        }
-      };
+        for (int i = 0; i < WIDE; ++i) sum += a[n][i] + b[n][i];
+      const float mean = group_sum(sum) * inv_d;
 #pragma unroll
       for (int n = 0; n < NU; ++n) {
-        affine(a[n], oa[n]);
-        affine(b[n], ob[n]);
+        const float ma = oa[n] >= 0 ? mean : 0.0f, mb = ob[n] >= 0 ? mean : 0.0f;
+#pragma unroll
+        for (int i = 0; i < WIDE; ++i) {
+          const bool there = VEC == WIDE || i < VEC || !rot[n];
+          a[n][i] -= there ? ma : 0.0f;
+          b[n][i] -= there ? mb : 0.0f;
+        }
       }
     }
+    float q = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NU; ++n) {
-      if (HALF) {
-        if (oa[n] >= 0 && oa[n] < half) {
+    for (int n = 0; n < NU; ++n)
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float c = cs[oa[n] + i], s = sn[oa[n] + i], t = a[n][i];
-            a[n][i] = t * c - b[n][i] * s;
-            b[n][i] = b[n][i] * c + t * s;
+      for (int i = 0; i < WIDE; ++i) q = fmaf(a[n][i], a[n][i], fmaf(b[n][i], b[n][i], q));
+    const float rstd = rsqrtf(fmaf(group_sum(q), inv_d, p.eps));  // within two units of 2^-24
+    if (live && pos[t] >= 0) {
+      const float* ct = cs + t * tl.row;
+      const float* st = sn + t * tl.row;
+#pragma unroll
+      for (int n = 0; n < NU; ++n) {
+        float wf[WIDE], bf[WIDE];
+        widen<E, WIDE>(wa[n], wf);
+        widen<E, WIDE>(ba[n], bf);
+#pragma unroll
+        for (int i = 0; i < WIDE; ++i) a[n][i] = fmaf(a[n][i] * rstd, wf[i], bf[i]);
+        widen<E, WIDE>(wb[n], wf);
+        widen<E, WIDE>(bb[n], bf);
+#pragma unroll
+        for (int i = 0; i < WIDE; ++i) b[n][i] = fmaf(b[n][i] * rstd, wf[i], bf[i]);
+        if constexpr (HALF) {
+          if (rot[n]) {
+            float co[VEC], si[VEC];
+            load_floats<VEC>(ct + oa[n], co);
+            load_floats<VEC>(st + oa[n], si);
+            rotate_halves<VEC>(a[n], b[n], co, si);
+          }
+        } else {
+          float co[4], si[4];
+          if (oa[n] >= 0 && oa[n] < p.R) {
+            load_floats<4>(ct + oa[n] / 2, co);
+            load_floats<4>(st + oa[n] / 2, si);
+            rotate_neighbours(a[n], co, si);
+          }
+          if (ob[n] >= 0 && ob[n] < p.R) {
+            load_floats<4>(ct + ob[n] / 2, co);
+            load_floats<4>(st + ob[n] / 2, si);
+            rotate_neighbours(b[n], co, si);
           }
         }
-      } else {
-        auto turn = [&](float (&v)[VEC], int off) {
-          if (off < 0 || off >= p.R) return;
-#pragma unroll
-          for (int i = 0; i < VEC; i += 2) {
-            const float c = cs[(off + i) / 2], s = sn[(off + i) / 2], t = v[i];
-            v[i] = t * c - v[i + 1] * s;
-            v[i + 1] = v[i + 1] * c + t * s;
-          }
-        };
-        turn(a[n], oa[n]);
-        turn(b[n], ob[n]);
+        uint32_t va[WIDE / 2], vb[WIDE / 2];
+        narrow<E, WIDE>(a[n], va);
+        narrow<E, WIDE>(b[n], vb);
+        if (VEC != TAIL && rot[n]) {
+          store_words<VEC>(out + oa[n], va);
+          store_words<VEC>(out + ob[n], vb);
+        } else {
+          if (oa[n] >= 0) store_words<TAIL>(out + oa[n], va);
+          if (ob[n] >= 0) store_words<TAIL>(out + ob[n], vb);
+        }
       }
-      if (oa[n] >= 0) store_vec<E, VEC>(dst + oa[n], a[n]);
-      if (ob[n] >= 0) store_vec<E, VEC>(dst + ob[n], b[n]);
     }
+    out += hd.out_token;
   }
 }
 
-// The widest vector that cuts both the rotated values (each half of them, in
-// the halves layout) and the rest into whole vectors.
-int vector_width(int layout, int D, int R) {
-  const int part = layout == ZQ_ROPE_HALF ? R / 2 : R;
-  for (int v = 8; v > 2; v /= 2)
-    if (part % v == 0 && (D - R) % v == 0) return v;
-  return 2;
-}
-
-template <typename E, bool HALF, bool NORM>
-cudaError_t launch_rope(const RopeParams& p0, int vec, cudaStream_t st) {
+template <typename E, int CUT, bool NORM>
+cudaError_t launch_cut(const RopeParams& p0, cudaStream_t st) {
+  using C = CutOf<CUT>;
   RopeParams p = p0;
-  p.units = (p.D / vec + 1) / 2;
+  const long long heads = static_cast<long long>(p.set[0].n) + p.set[1].n;
   int lanes = 1;
-  while (lanes < p.units && lanes < 32) lanes *= 2;
-  const int heads = p.q.n + p.k.n, groups = kThreads / lanes;
-  // With enough tokens one CTA has all heads of a token (the sines are then
-  // computed once per token); with fewer, the heads are spread over CTAs
-  // until the SMs are busy.
-  const int turns = (heads + groups - 1) / groups;
-  int chunks = 1;
-  while (chunks < turns && static_cast<long long>(p.T) * chunks < 4ll * num_sms()) chunks *= 2;
-  p.per_chunk = (turns + chunks - 1) / chunks * groups;
-  p.chunks = (heads + p.per_chunk - 1) / p.per_chunk;
-  const long long ctas = static_cast<long long>(p.T) * p.chunks;
+  while (lanes < NormCut<CUT>::units(p.D, p.R) && lanes < 32) lanes *= 2;
+  const long long threads =
+      NORM ? heads * lanes
+           : heads * (C::rotated_units(p.R) + (p.copy_rest ? C::tail_units(p.D, p.R) : 0));
+  constexpr int cta = NORM ? kNormThreads : kThreads;
+  const long long columns = (threads + cta - 1) / cta;
+  // As many tokens to a CTA as leave so many CTAs for each SM (their sines
+  // have to fit).  Measured: 4096 tokens of 2 x 64 heads of 96 values, no norm,
+  // 4, 16 and 24 per SM: 46.8, 40.9 and 37.2 us, but 8192 tokens of 2 x 16
+  // heads of 80 best with 16 (19.5 us); with a norm, 2011 tokens of 40 heads
+  // of 128 in CTAs of 256, 128 and 64 threads: 17.7, 13.3 and 12.9 us.
+  const int row = std::max(4, (p.R / 2 + 3) & ~3);
+  const long long want = (NORM ? 16ll : 20ll) * num_sms();
+  p.tokens = static_cast<int>(
+      std::max(1ll, std::min<long long>(p.T * columns / want, std::min(kMaxTokens, kMaxAngles / row))));
+  const long long ctas = (static_cast<long long>(p.T) + p.tokens - 1) / p.tokens * columns;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-  auto go = [&](auto* kernel) {
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, p, lanes);
-  };
-  switch (vec) {
-    case 8: return go(qk_rope_kernel<E, 8, 1, HALF, NORM>);
-    case 4: return go(qk_rope_kernel<E, 4, 1, HALF, NORM>);
-    default: return go(qk_rope_kernel<E, 2, 2, HALF, NORM>);
-  }
+  p.columns = static_cast<int>(columns);
+  const dim3 grid(static_cast<unsigned>(ctas));
+  if (NORM) return launch_pdl(norm_rope_kernel<E, CUT>, grid, dim3(cta), 0, st, p, lanes);
+  return launch_pdl(rope_kernel<E, CUT>, grid, dim3(cta), 0, st, p);
+}
+
+template <typename E, bool NORM>
+cudaError_t launch_rope(const RopeParams& p, int layout, cudaStream_t st) {
+  if (layout == ZQ_ROPE_INTERLEAVED) return launch_cut<E, kNeighbours, NORM>(p, st);
+  if (p.R / 2 % 8 == 0) return launch_cut<E, kHalf8, NORM>(p, st);
+  if (p.R / 2 % 4 == 0) return launch_cut<E, kHalf4, NORM>(p, st);
+  return launch_cut<E, kHalf2, NORM>(p, st);
 }
 
 // The checks of one of the two head sets; *out is only filled when it is fine.
@@ -309,9 +501,9 @@ extern "C" zq_status zq_qk_norm_rope(const zq_heads* q, const zq_heads* k, int d
   if (layout == ZQ_ROPE_HALF && R % 4 != 0) return ZQ_ERR_SHAPE;
   if (!q) return ZQ_ERR_NULL;
   RopeParams p{};
-  zq_status rc = check_heads(q, T, D, &p.q);
-  if (rc == ZQ_OK && k) rc = check_heads(k, T, D, &p.k);
-  if (rc != ZQ_OK || T == 0 || p.q.n + p.k.n == 0) return rc;
+  zq_status rc = check_heads(q, T, D, &p.set[0]);
+  if (rc == ZQ_OK && k) rc = check_heads(k, T, D, &p.set[1]);
+  if (rc != ZQ_OK || T == 0 || p.set[0].n + p.set[1].n == 0) return rc;
   if (!positions || (R > 0 && !inv_freq)) return ZQ_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(positions) % 4 || reinterpret_cast<uintptr_t>(inv_freq) % 4)
     return ZQ_ERR_ALIGN;
@@ -324,17 +516,15 @@ extern "C" zq_status zq_qk_norm_rope(const zq_heads* q, const zq_heads* k, int d
   p.scale = scale;
   p.eps = eps;
   // in place and without a norm, the values behind R stay as they are
-  p.copy_rest = norm != ZQ_NORM_NONE || (p.q.n && p.q.in != p.q.out) || (p.k.n && p.k.in != p.k.out);
-  if (!p.copy_rest && R == 0) return ZQ_OK;
-  const int vec = vector_width(layout, D, R);
+  p.copy_rest = norm != ZQ_NORM_NONE;
+  for (const Heads& h : p.set)
+    if (h.n && h.in != h.out) p.copy_rest = 1;
+  if (!p.copy_rest && R == 0) return ZQ_OK;  // nothing changes
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = with_dtype(dtype, [&](auto tag) {
     using E = decltype(tag);
-    if (layout == ZQ_ROPE_HALF)
-      return norm == ZQ_NORM_NONE ? launch_rope<E, true, false>(p, vec, st)
-                                  : launch_rope<E, true, true>(p, vec, st);
-    return norm == ZQ_NORM_NONE ? launch_rope<E, false, false>(p, vec, st)
-                                : launch_rope<E, false, true>(p, vec, st);
+    return norm == ZQ_NORM_NONE ? launch_rope<E, false>(p, layout, st)
+                                : launch_rope<E, true>(p, layout, st);
   });
   return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
 }
