@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -28,15 +29,6 @@ EXPORTS = (
     "zq_widen_int4_weights", "zq_quantize_weights_fp8", "zq_ln_quant_fp8", "zq_bias_act_quant_fp8",
     "zq_gemm_fp8", "zq_qk_norm_rope", "zq_rope_frequencies",
 )
-
-
-class Heads(ctypes.Structure):
-    """zq_heads: query or key heads in a strided tensor."""
-
-    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
-                ("bias", ctypes.c_void_p), ("in_token_stride", ctypes.c_longlong),
-                ("in_head_stride", ctypes.c_longlong), ("out_token_stride", ctypes.c_longlong),
-                ("out_head_stride", ctypes.c_longlong), ("heads", ctypes.c_int)]
 
 
 class ZQError(RuntimeError):
@@ -74,8 +66,7 @@ def _load():
         "zq_ln_quant_fp8": ([P, I, P, P, I, I, F, P, P, P, P], I),
         "zq_bias_act_quant_fp8": ([P, I, P, I, I, I, P, P, P, P], I),
         "zq_gemm_fp8": ([P, P, P, P, P, I, I, I, I, P, P], I),
-        "zq_qk_norm_rope": ([ctypes.POINTER(Heads), ctypes.POINTER(Heads), I, I, I, I, F, P, P, I,
-                             I, F, P], I),
+        "zq_qk_norm_rope": ([P, P, I, I, I, I, F, P, P, I, I, F, P], I),
         "zq_rope_frequencies": ([I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double,
                                  ctypes.c_double, I, ctypes.POINTER(F), ctypes.POINTER(F)], I),
     }
@@ -312,59 +303,82 @@ def gemm_w4a16(X, Wq4, s_grp, bias=None, Y=None, acc_dbg=None, stream=None):
 
 
 # ------------------------------------------------- block-scaled FP8 (e4m3)
+#
+# The calls below serve single tokens too, where a kernel takes two or three
+# microseconds: their checks take one fast path per tensor, and build the
+# message of a refusal only when there is one.
 
 FP8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # zq_dtype
+_F32, _I32 = torch.float32, torch.int32
+_current_device = torch.cuda.current_device
 
 
 def _blocks(n: int) -> int:
     return -(-n // FP8_BLOCK)
 
 
-def _dtype16(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
+def _raw_stream(stream, dev: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
+    return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _ptr(t, dtype, shape, name: str, dev: int):
+    """The data pointer of a contiguous tensor of this dtype and shape on the
+    current device `dev` (the kernels run there); None stays None."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == dev):
+        return t.data_ptr()
+    _dev(t, dtype, shape, name)
+    raise ValueError(f"{name} must be on the current device cuda:{dev}, got {t.device}")
+
+
+def _matrix(t, name: str):
+    """(dtype code, rows, columns) of a 16-bit matrix."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
-    return d
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    return d, rows, cols
 
 
-def _same_device(*tensors):
-    """The kernels run on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got {t.device}")
+def _fp8_out(X, rows, cols, scale_rows, Xq, s_blk, names, dev):
+    """Codes and scales (made where not given) and their pointers."""
+    scales = (scale_rows, -(-cols // FP8_BLOCK))
+    if Xq is None:
+        Xq = torch.empty_like(X, dtype=FP8, memory_format=torch.contiguous_format)
+        q = Xq.data_ptr()
+    else:
+        q = _ptr(Xq, FP8, (rows, cols), names[0], dev)
+    if s_blk is None:
+        s_blk = X.new_empty(scales, dtype=_F32)
+        s = s_blk.data_ptr()
+    else:
+        s = _ptr(s_blk, _F32, scales, names[1], dev)
+    return Xq, s_blk, q, s
 
 
 def quantize_weights_fp8(W: torch.Tensor, Wq=None, s_blk=None, stream=None):
     """Weights [N,K] (fp16 or bf16) to e4m3 with one scale for each 128 x 128
     block (zq_quantize_weights_fp8).  Returns (Wq float8_e4m3fn [N,K],
     s_blk fp32 [ceil(N/128), ceil(K/128)])."""
-    N, K = W.shape
-    dt = _dtype16(W, "W")
-    w = _dev(W, W.dtype, (N, K), "W")
-    if Wq is None:
-        Wq = torch.empty((N, K), dtype=FP8, device=W.device)
-    blocks = (_blocks(N), _blocks(K))
-    if s_blk is None:
-        s_blk = torch.empty(blocks, dtype=torch.float32, device=W.device)
-    args = (w, dt, N, K, _dev(Wq, FP8, (N, K), "Wq"), _dev(s_blk, torch.float32, blocks, "s_blk"))
-    _same_device(W, Wq, s_blk)
-    _check(_lib.zq_quantize_weights_fp8(*args, _stream(stream)), "zq_quantize_weights_fp8")
+    dt, N, K = _matrix(W, "W")
+    dev = _current_device()
+    w = _ptr(W, W.dtype, (N, K), "W", dev)
+    Wq, s_blk, q, s = _fp8_out(W, N, K, _blocks(N), Wq, s_blk, ("Wq", "s_blk"), dev)
+    rc = _lib.zq_quantize_weights_fp8(w, dt, N, K, q, s, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "zq_quantize_weights_fp8")
     return Wq, s_blk
-
-
-def _fp8_rows(X, Xq, s_blk):
-    T, K = X.shape
-    if Xq is None:
-        Xq = torch.empty((T, K), dtype=FP8, device=X.device)
-    blocks = (T, _blocks(K))
-    if s_blk is None:
-        s_blk = torch.empty(blocks, dtype=torch.float32, device=X.device)
-    return T, K, Xq, s_blk, _dev(Xq, FP8, (T, K), "Xq"), _dev(s_blk, torch.float32, blocks, "s_blk")
 
 
 def ln_quant_fp8(X: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, Xq=None, s_blk=None,
@@ -373,13 +387,15 @@ def ln_quant_fp8(X: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, Xq=N
     each 128 values (zq_ln_quant_fp8); gamma=None is quant-only.  X, gamma,
     beta and y_ln share one dtype, fp16 or bf16.  Returns (Xq float8_e4m3fn
     [T,K], s_blk fp32 [T, ceil(K/128)])."""
-    dt = _dtype16(X, "X")
-    x = _dev(X, X.dtype, tuple(X.shape), "X")
-    T, K, Xq, s_blk, xq, sb = _fp8_rows(X, Xq, s_blk)
-    args = (x, dt, _dev(gamma, X.dtype, (K,), "gamma"), _dev(beta, X.dtype, (K,), "beta"), T, K,
-            float(eps), xq, sb, _dev(y_ln, X.dtype, (T, K), "Y_ln"))
-    _same_device(X, gamma, beta, Xq, s_blk, y_ln)
-    _check(_lib.zq_ln_quant_fp8(*args, _stream(stream)), "zq_ln_quant_fp8")
+    dt, T, K = _matrix(X, "X")
+    e, dev = X.dtype, _current_device()
+    x = _ptr(X, e, (T, K), "X", dev)
+    g, b = _ptr(gamma, e, (K,), "gamma", dev), _ptr(beta, e, (K,), "beta", dev)
+    y = _ptr(y_ln, e, (T, K), "Y_ln", dev)
+    Xq, s_blk, q, s = _fp8_out(X, T, K, T, Xq, s_blk, ("Xq", "s_blk"), dev)
+    rc = _lib.zq_ln_quant_fp8(x, dt, g, b, T, K, eps, q, s, y, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "zq_ln_quant_fp8")
     return Xq, s_blk
 
 
@@ -388,32 +404,42 @@ def bias_act_quant_fp8(X: torch.Tensor, bias=None, act: int = ACT_NONE, Xq=None,
     """e4m3 quantization of token rows fused into a bias-add (act=ACT_NONE) or
     a bias-add and GeLU (act=ACT_GELU) (zq_bias_act_quant_fp8).  Returns as
     ln_quant_fp8; y, if given, receives the activation."""
-    dt = _dtype16(X, "X")
-    x = _dev(X, X.dtype, tuple(X.shape), "X")
-    T, K, Xq, s_blk, xq, sb = _fp8_rows(X, Xq, s_blk)
-    args = (x, dt, _dev(bias, X.dtype, (K,), "bias"), T, K, int(act), xq, sb,
-            _dev(y, X.dtype, (T, K), "Y_act"))
-    _same_device(X, bias, Xq, s_blk, y)
-    _check(_lib.zq_bias_act_quant_fp8(*args, _stream(stream)), "zq_bias_act_quant_fp8")
+    dt, T, K = _matrix(X, "X")
+    e, dev = X.dtype, _current_device()
+    x, b = _ptr(X, e, (T, K), "X", dev), _ptr(bias, e, (K,), "bias", dev)
+    ya = _ptr(y, e, (T, K), "Y_act", dev)
+    Xq, s_blk, q, s = _fp8_out(X, T, K, T, Xq, s_blk, ("Xq", "s_blk"), dev)
+    rc = _lib.zq_bias_act_quant_fp8(x, dt, b, T, K, act, q, s, ya, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "zq_bias_act_quant_fp8")
     return Xq, s_blk
 
 
 def gemm_fp8(Xq, s_x, Wq, s_w, bias=None, Y=None, out_dtype=torch.float16, stream=None):
     """Y = (s_x Xq) (s_w Wq)^T + bias on block-scaled e4m3 codes
     (zq_gemm_fp8); Y and bias are of out_dtype, fp16 or bf16."""
-    if out_dtype not in _DTYPES:
+    dt = _DTYPES.get(out_dtype)
+    if dt is None:
         raise TypeError(f"out_dtype must be torch.float16 or torch.bfloat16, got {out_dtype}")
+    for t, name in ((Xq, "Xq"), (Wq, "Wq")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dim() != 2:
+            raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
     T, K = Xq.shape
     N = Wq.shape[0]
+    kb, dev = -(-K // FP8_BLOCK), _current_device()
+    x, sx = _ptr(Xq, FP8, (T, K), "Xq", dev), _ptr(s_x, _F32, (T, kb), "s_x", dev)
+    w, sw = _ptr(Wq, FP8, (N, K), "Wq", dev), _ptr(s_w, _F32, (_blocks(N), kb), "s_w", dev)
+    b = _ptr(bias, out_dtype, (N,), "bias", dev)
     if Y is None:
-        Y = torch.empty((T, N), dtype=out_dtype, device=Xq.device)
-    kb = _blocks(K)
-    args = (_dev(Xq, FP8, (T, K), "Xq"), _dev(s_x, torch.float32, (T, kb), "s_x"),
-            _dev(Wq, FP8, (N, K), "Wq"), _dev(s_w, torch.float32, (_blocks(N), kb), "s_w"),
-            _dev(bias, out_dtype, (N,), "bias"), T, N, K, _DTYPES[out_dtype],
-            _dev(Y, out_dtype, (T, N), "Y"))
-    _same_device(Xq, s_x, Wq, s_w, bias, Y)
-    _check(_lib.zq_gemm_fp8(*args, _stream(stream)), "zq_gemm_fp8")
+        Y = Xq.new_empty((T, N), dtype=out_dtype)
+        y = Y.data_ptr()
+    else:
+        y = _ptr(Y, out_dtype, (T, N), "Y", dev)
+    rc = _lib.zq_gemm_fp8(x, sx, w, sw, b, T, N, K, dt, y, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "zq_gemm_fp8")
     return Y
 
 
@@ -422,6 +448,7 @@ def gemm_fp8(Xq, s_x, Wq, s_w, bias=None, Y=None, out_dtype=torch.float16, strea
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
+_pack_heads = struct.Struct("@PPPPqqqqi4x").pack  # zq_heads
 
 
 def rope_frequencies(R: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
@@ -437,26 +464,35 @@ def rope_frequencies(R: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, f
     return torch.tensor(list(f), dtype=torch.float32), float(scale.value)
 
 
-def _heads(t, out, weight, bias, T, D, dtype, name):
-    """(zq_heads, out) of a strided [T, heads, D] tensor."""
+def _heads(t, out, weight, bias, T, D, dtype, name, dev):
+    """(zq_heads as bytes, out) of a strided [T, heads, D] tensor."""
+    H = t.shape[1] if isinstance(t, torch.Tensor) and t.dim() == 3 else -1
     for what, v in ((name, t), (name + "_out", out)):
         if v is None:
             continue
         if not isinstance(v, torch.Tensor) or not v.is_cuda:
             raise TypeError(f"{what} must be a CUDA tensor")
-        if v.dtype != dtype:
+        if v.dtype is not dtype:
             raise TypeError(f"{what} must be {dtype}, got {v.dtype}")
-        if v.dim() != 3 or v.shape[0] != T or v.shape[1] != t.shape[1] or v.shape[2] != D:
-            raise ValueError(f"{what} must have shape ({T}, {t.shape[1]}, {D}), got {tuple(v.shape)}")
+        if v.shape != (T, H, D):
+            raise ValueError(f"{what} must have shape ({T}, {'heads' if H < 0 else H}, {D}), "
+                             f"got {tuple(v.shape)}")
         if D > 1 and v.stride(2) != 1:
             raise ValueError(f"the values of a head of {what} must be contiguous")
+        if v.get_device() != dev:
+            raise ValueError(f"{what} must be on the current device cuda:{dev}, got {v.device}")
     if out is None:
-        out = torch.empty(t.shape, dtype=dtype, device=t.device)
+        out = torch.empty_like(t, memory_format=torch.contiguous_format)
     # strides of dimensions of one element mean nothing and may be anything
-    st = [0 if v.shape[d] <= 1 else v.stride(d) for v in (t, out) for d in (0, 1)]
-    h = Heads(t.data_ptr(), out.data_ptr(), _dev(weight, dtype, (D,), name + "_weight"),
-              _dev(bias, dtype, (D,), name + "_bias"), *st, t.shape[1])
-    return h, out
+    a, b = t.stride(), out.stride()
+    it, ih, ot, oh = a[0], a[1], b[0], b[1]
+    if T <= 1:
+        it = ot = 0
+    if H <= 1:
+        ih = oh = 0
+    return _pack_heads(t.data_ptr(), out.data_ptr(),
+                       _ptr(weight, dtype, (D,), name + "_weight", dev) or 0,
+                       _ptr(bias, dtype, (D,), name + "_bias", dev) or 0, it, ih, ot, oh, H), out
 
 
 def qk_norm_rope(q, k, positions, inv_freq, layout: int = ROPE_HALF, scale: float = 1.0,
@@ -469,20 +505,30 @@ def qk_norm_rope(q, k, positions, inv_freq, layout: int = ROPE_HALF, scale: floa
     the device (negative: the row is skipped), inv_freq fp32 [R/2] (R values of
     a head are rotated).  q_out=q works in place; without q_out a new tensor is
     made (its skipped rows are undefined).  Returns (q_out, k_out)."""
-    dt = _dtype16(q, "q")
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    e = q.dtype
+    dt = _DTYPES.get(e)
+    if dt is None:
+        raise TypeError(f"q must be torch.float16 or torch.bfloat16, got {e}")
     if q.dim() != 3:
         raise ValueError(f"q must have shape (tokens, heads, head_dim), got {tuple(q.shape)}")
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a tensor of one dimension")
     T, _, D = q.shape
-    hq, q_out = _heads(q, q_out, q_weight, q_bias, T, D, q.dtype, "q")
+    half, dev = inv_freq.shape[0], _current_device()
+    pos = _ptr(positions, _I32, (T,), "positions", dev)
+    f = _ptr(inv_freq, _F32, (half,), "inv_freq", dev)
+    if pos is None:
+        raise TypeError("positions must be a CUDA tensor")
+    hq, q_out = _heads(q, q_out, q_weight, q_bias, T, D, e, "q", dev)
     hk = None
     if k is not None:
-        hk, k_out = _heads(k, k_out, k_weight, k_bias, T, D, q.dtype, "k")
-    half = inv_freq.shape[0]
-    args = (dt, T, D, int(norm), float(eps), _dev(positions, torch.int32, (T,), "positions"),
-            _dev(inv_freq, torch.float32, (half,), "inv_freq"), 2 * half, int(layout), float(scale))
-    _same_device(q, k, positions, inv_freq, q_weight, q_bias, k_weight, k_bias, q_out, k_out)
-    _check(_lib.zq_qk_norm_rope(ctypes.byref(hq), None if hk is None else ctypes.byref(hk), *args,
-                                _stream(stream)), "zq_qk_norm_rope")
+        hk, k_out = _heads(k, k_out, k_weight, k_bias, T, D, e, "k", dev)
+    rc = _lib.zq_qk_norm_rope(hq, hk, dt, T, D, norm, eps, pos, f, 2 * half, layout, scale,
+                              _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "zq_qk_norm_rope")
     return q_out, k_out
 
 
