@@ -504,7 +504,11 @@ struct TileCfg {
   static constexpr int ROWS_PER_HALF = W_ROWS / HALVES;  // weight rows of one MMA in this CTA
   static constexpr int A_BYTES = BM * BK, B_BYTES = W_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int XCHG_BYTES = SPLIT ? BM * BN * 4 : 0;  // partial sums of the other CTAs
+  // partial sums from all CTAs of a cluster: S * ceil(16 / S) float4 for each
+  // accumulating thread, at most 21 (S = 7)
+  static constexpr int PIECES = COLS / 4;
+  static constexpr int XCHG_BYTES = SPLIT ? 21 * 32 * kAccWarps * 16 : 0;
+  static_assert(!SPLIT || PIECES == 16, "room for the partial sums");
   static constexpr int AUX_BYTES = 2 * kGroupBytes + 2 * BN * 2;  // two scale groups, two units' bias
   static constexpr int STAGES_RAW =
       (kTileSmem - 1536 - XCHG_BYTES - AUX_BYTES) / STAGE_BYTES;
@@ -932,19 +936,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         slot ^= 1;
         sphase ^= slot == 0;
       } else {
-        // Column chunk j (COLS / csize columns of each warp) goes to CTA j,
-        // as float4 [source][piece][thread]: neighbouring lanes, neighbouring
-        // 16-byte words.
-        const int tid = threadIdx.x - 32 * kAccWarp0;
-        const int pieces = COLS / 4 / static_cast<int>(csize);
+        // Four columns at a time, in turn to the CTAs of the cluster, as float4
+        // [source][turn][thread]: neighbouring lanes, neighbouring words.
+        const int tid = threadIdx.x - 32 * kAccWarp0, S = static_cast<int>(csize);
+        const int turns = (C::PIECES + S - 1) / S;
         const uint32_t xchg = smem_u32(smem + C::OFF_XCHG);
+        int to = 0, turn = 0;
 #pragma unroll
-        for (int i = 0; i < COLS / 4; ++i) {
-          const int to = i / pieces, piece = i - to * pieces;
+        for (int i = 0; i < C::PIECES; ++i) {
           const float2 a = unpack_f32x2(acc[2 * i]), b = unpack_f32x2(acc[2 * i + 1]);
-          st_cluster_v4(
-              mapa_shared(xchg + (((static_cast<int>(rank) * pieces + piece) * (32 * kAccWarps) + tid) << 4), to),
-              make_float4(a.x, a.y, b.x, b.y));
+          const int at = (static_cast<int>(rank) * turns + turn) * (32 * kAccWarps) + tid;
+          st_cluster_v4(mapa_shared(xchg + (static_cast<uint32_t>(at) << 4), to),
+                        make_float4(a.x, a.y, b.x, b.y));
+          if (++to == S) {
+            to = 0;
+            ++turn;
+          }
         }
       }
     }
@@ -955,26 +962,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     cluster_sync_all();  // all partial sums have arrived
     if (warp >= kAccWarp0) {
       const int quad = warp & 3, part = (warp - kAccWarp0) >> 2;
-      const int tid = threadIdx.x - 32 * kAccWarp0;
-      const int cols = COLS / static_cast<int>(csize), pieces = cols / 4;
+      const int tid = threadIdx.x - 32 * kAccWarp0, S = static_cast<int>(csize);
+      const int turns = (C::PIECES + S - 1) / S;
       int m, n;
       tile_of(unit0, p, m, n);
       const int t = m * BM + quad * 32 + lane;
-      const int o0 = n * C::BN + part * COLS + static_cast<int>(rank) * cols;
-      const float4* in = reinterpret_cast<const float4*>(smem + C::OFF_XCHG);
+      const int o0 = n * C::BN + part * COLS;
+      const float4* in = reinterpret_cast<const float4*>(smem + C::OFF_XCHG) + tid;
       E* y = static_cast<E*>(p.Y) + static_cast<size_t>(t) * p.N + o0;
       const E* bias = static_cast<const E*>(p.bias);
-      for (int c = 0; c < cols; c += 8) {
-        if (t >= p.T || o0 + c >= p.N) break;
-        float v[8] = {};
-        for (uint32_t src = 0; src < csize; ++src) {
-          const float4 a = in[(src * pieces + c / 4) * (32 * kAccWarps) + tid];
-          const float4 b = in[(src * pieces + c / 4 + 1) * (32 * kAccWarps) + tid];
-          v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-          v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      for (int turn = 0; turn < turns; ++turn) {
+        const int c = 4 * (turn * S + static_cast<int>(rank));
+        if (c >= COLS || t >= p.T || o0 + c >= p.N) break;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int src = 0; src < S; ++src) {
+          const float4 a = in[(src * turns + turn) * (32 * kAccWarps)];
+          v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
         }
-        if (bias) add_bias<E>(v, __ldg(reinterpret_cast<const uint4*>(bias + o0 + c)));
-        *reinterpret_cast<uint4*>(y + c) = pack8<E>(v);
+        if (bias) {
+          const uint2 b = __ldg(reinterpret_cast<const uint2*>(bias + o0 + c));
+          const float2 b0 = unpack2<E>(b.x), b1 = unpack2<E>(b.y);
+          v.x += b0.x, v.y += b0.y, v.z += b1.x, v.w += b1.y;
+        }
+        *reinterpret_cast<uint2*>(y + c) = make_uint2(pack2<E>(v.x, v.y), pack2<E>(v.z, v.w));
       }
     }
   }
@@ -1039,7 +1049,45 @@ cudaError_t launch_tile(const Fp8Params& p, int split, int* status, cudaStream_t
   return launch_pdl(kernel, dim3(grid), dim3(kTileThreads), C::SMEM_BYTES, st, mx, mw, tp);
 }
 
-// The tile for many tokens, from the number of waves that each tiling needs.
+// Clusters of S CTAs of the split tile that fit the current device at once
+// (asked once per size and device).
+template <typename E>
+cudaError_t split_clusters(int S, int* out) {
+  using C = TileCfg<128, false, true>;
+  auto* kernel = fp8_tile_kernel<E, C>;
+  static std::atomic<int> known[64][9];
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev < 64 ? known[dev][S].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    e = allow_smem(kernel, C::SMEM_BYTES, ready);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S * 64);
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    n = std::max(n, 1);
+    if (dev < 64) known[dev][S].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
+// The tiling for many tokens: the least of these estimates (us), fitted to 40
+// shapes of 65 to 4096 tokens.  A tile costs so much per scale block (bound
+// by the copies into an SM, which a row pitch that is no multiple of 128
+// bytes doubles in lines) and for its output; a split tile some more for the
+// exchange.
 template <typename E>
 cudaError_t launch_tiles(const Fp8Params& p, cudaStream_t st) {
   int* status = device_status_ptr();
@@ -1050,25 +1098,47 @@ cudaError_t launch_tiles(const Fp8Params& p, cudaStream_t st) {
   auto tiles = [&](int tm, int tn) {
     return static_cast<long long>((p.T - 1) / tm + 1) * ((p.N - 1) / tn + 1);
   };
-  const long long small = tiles(BM, 128);
-  // few tiles: share each along K, at least four blocks to a CTA
-  int split = 1;
-  while (split < 8 && small * split * 2 <= sms && p.kblocks >= split * 2 * 4) split *= 2;
-  if (fsplit) split = fsplit;
-  if (split > 1 && !fpair && !fbn) {
-    while (split & (split - 1)) --split;  // the tiles' columns are shared out evenly
-    return launch_tile<E, TileCfg<128, false, true>>(p, split, status, st);
+  const bool aligned = p.K % kFp8Block == 0;
+  struct Option {
+    int bn, pair;
+    double per_block, per_tile;  // (per block with one wave: at most 0.46)
+  };
+  const Option options[4] = {{128, 0, aligned ? 0.39 : 0.52, 1.6},
+                             {128, 1, 0.50, 2.0},
+                             {256, 0, aligned ? 0.60 : 0.85, 2.2},
+                             {256, 1, 0.56, 2.1}};
+  double best = 1e30;
+  const Option* pick = nullptr;
+  for (const Option& o : options) {
+    if ((fbn && o.bn != fbn) || (fpair ? o.pair != fpair - 1 : o.pair && p.T <= BM)) continue;
+    const long long at_once = o.pair ? sms / 2 : sms;
+    const long long waves = (tiles(o.pair ? 2 * BM : BM, o.bn) + at_once - 1) / at_once;
+    const double per_block = waves == 1 ? std::min(o.per_block, o.bn == 128 ? 0.46 : 1.0) : o.per_block;
+    const double cost = static_cast<double>(waves) * (p.kblocks * per_block + o.per_tile);
+    if (cost < best) best = cost, pick = &o;
   }
-  // cost of a tiling: waves x columns per CTA
-  const long long c128 = (small + sms - 1) / sms * 128;
-  const long long c256 = (tiles(BM, 256) + sms - 1) / sms * 256;
-  const long long cpair = (tiles(2 * BM, 256) + sms / 2 - 1) / (sms / 2) * 256;
-  int pair = fpair ? fpair - 1 : cpair <= std::min(c128, c256);
-  int bn = fbn ? fbn : (pair ? 256 : (c256 <= c128 ? 256 : 128));
-  if (pair && bn == 256) return launch_tile<E, TileCfg<256, true, false>>(p, 1, status, st);
-  if (pair) return launch_tile<E, TileCfg<128, true, false>>(p, 1, status, st);
-  if (bn == 256) return launch_tile<E, TileCfg<256, false, false>>(p, 1, status, st);
-  return launch_tile<E, TileCfg<128, false, false>>(p, 1, status, st);
+  // few tiles: share each along K, at least three blocks to a CTA
+  int split = 1;
+  const long long small = tiles(BM, 128);
+  if (fsplit > 1) {
+    split = fsplit;
+  } else if (fsplit == 0 && !fbn && !fpair && small * 2 <= sms) {
+    for (int S = 2; S <= 8 && p.kblocks >= 3 * S; ++S) {
+      int clusters = 0;
+      const cudaError_t e = split_clusters<E>(S, &clusters);
+      if (e != cudaSuccess) return e;
+      if (small > clusters) continue;
+      const double cost =
+          (p.kblocks + S - 1) / S * (aligned ? 0.40 : 0.46) + 1.6 + 4.0;
+      if (cost < best) best = cost, split = S;
+    }
+  }
+  if (split > 1) return launch_tile<E, TileCfg<128, false, true>>(p, split, status, st);
+  if (pick->bn == 256)
+    return pick->pair ? launch_tile<E, TileCfg<256, true, false>>(p, 1, status, st)
+                      : launch_tile<E, TileCfg<256, false, false>>(p, 1, status, st);
+  return pick->pair ? launch_tile<E, TileCfg<128, true, false>>(p, 1, status, st)
+                    : launch_tile<E, TileCfg<128, false, false>>(p, 1, status, st);
 }
 
 }  // namespace
