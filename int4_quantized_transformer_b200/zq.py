@@ -311,19 +311,11 @@ def gemm_w4a16(X, Wq4, s_grp, bias=None, Y=None, acc_dbg=None, stream=None):
 FP8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # zq_dtype
-_F32, _I32 = torch.float32, torch.int32
-_current_device = torch.cuda.current_device
-
-
-def _blocks(n: int) -> int:
-    return -(-n // FP8_BLOCK)
-
-
-def _raw_stream(stream, dev: int) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
-    return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
+_F32, _I32, _CONTIGUOUS = torch.float32, torch.int32, torch.contiguous_format
+# the plain getters behind torch.cuda.current_device() and current_stream()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _ptr(t, dtype, shape, name: str, dev: int):
@@ -339,31 +331,34 @@ def _ptr(t, dtype, shape, name: str, dev: int):
 
 
 def _matrix(t, name: str):
-    """(dtype code, rows, columns) of a 16-bit matrix."""
+    """(pointer, zq_dtype, rows, columns, device) of a 16-bit matrix."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    rows, cols = t.shape
-    return d, rows, cols
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(shape)}")
+    dev = _current_device()
+    if not t.is_contiguous() or t.get_device() != dev:
+        _ptr(t, t.dtype, shape, name, dev)
+    return t.data_ptr(), d, shape[0], shape[1], dev
 
 
-def _fp8_out(X, rows, cols, scale_rows, Xq, s_blk, names, dev):
+def _fp8_out(X, rows, cols, scale_rows, Xq, s_blk, dev):
     """Codes and scales (made where not given) and their pointers."""
-    scales = (scale_rows, -(-cols // FP8_BLOCK))
+    kb = -(-cols // FP8_BLOCK)
     if Xq is None:
-        Xq = torch.empty_like(X, dtype=FP8, memory_format=torch.contiguous_format)
+        Xq = torch.empty_like(X, dtype=FP8, memory_format=_CONTIGUOUS)
         q = Xq.data_ptr()
     else:
-        q = _ptr(Xq, FP8, (rows, cols), names[0], dev)
+        q = _ptr(Xq, FP8, (rows, cols), "Xq" if rows == scale_rows else "Wq", dev)
     if s_blk is None:
-        s_blk = X.new_empty(scales, dtype=_F32)
+        s_blk = torch.empty_strided((scale_rows, kb), (kb, 1), dtype=_F32, device=X.device)
         s = s_blk.data_ptr()
     else:
-        s = _ptr(s_blk, _F32, scales, names[1], dev)
+        s = _ptr(s_blk, _F32, (scale_rows, kb), "s_blk", dev)
     return Xq, s_blk, q, s
 
 
@@ -371,11 +366,10 @@ def quantize_weights_fp8(W: torch.Tensor, Wq=None, s_blk=None, stream=None):
     """Weights [N,K] (fp16 or bf16) to e4m3 with one scale for each 128 x 128
     block (zq_quantize_weights_fp8).  Returns (Wq float8_e4m3fn [N,K],
     s_blk fp32 [ceil(N/128), ceil(K/128)])."""
-    dt, N, K = _matrix(W, "W")
-    dev = _current_device()
-    w = _ptr(W, W.dtype, (N, K), "W", dev)
-    Wq, s_blk, q, s = _fp8_out(W, N, K, _blocks(N), Wq, s_blk, ("Wq", "s_blk"), dev)
-    rc = _lib.zq_quantize_weights_fp8(w, dt, N, K, q, s, _raw_stream(stream, dev))
+    w, dt, N, K, dev = _matrix(W, "W")
+    Wq, s_blk, q, s = _fp8_out(W, N, K, -(-N // FP8_BLOCK), Wq, s_blk, dev)
+    rc = _lib.zq_quantize_weights_fp8(
+        w, dt, N, K, q, s, _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "zq_quantize_weights_fp8")
     return Wq, s_blk
@@ -387,13 +381,14 @@ def ln_quant_fp8(X: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, Xq=N
     each 128 values (zq_ln_quant_fp8); gamma=None is quant-only.  X, gamma,
     beta and y_ln share one dtype, fp16 or bf16.  Returns (Xq float8_e4m3fn
     [T,K], s_blk fp32 [T, ceil(K/128)])."""
-    dt, T, K = _matrix(X, "X")
-    e, dev = X.dtype, _current_device()
-    x = _ptr(X, e, (T, K), "X", dev)
-    g, b = _ptr(gamma, e, (K,), "gamma", dev), _ptr(beta, e, (K,), "beta", dev)
-    y = _ptr(y_ln, e, (T, K), "Y_ln", dev)
-    Xq, s_blk, q, s = _fp8_out(X, T, K, T, Xq, s_blk, ("Xq", "s_blk"), dev)
-    rc = _lib.zq_ln_quant_fp8(x, dt, g, b, T, K, eps, q, s, y, _raw_stream(stream, dev))
+    x, dt, T, K, dev = _matrix(X, "X")
+    e = X.dtype
+    g = None if gamma is None else _ptr(gamma, e, (K,), "gamma", dev)
+    b = None if beta is None else _ptr(beta, e, (K,), "beta", dev)
+    y = None if y_ln is None else _ptr(y_ln, e, (T, K), "Y_ln", dev)
+    Xq, s_blk, q, s = _fp8_out(X, T, K, T, Xq, s_blk, dev)
+    rc = _lib.zq_ln_quant_fp8(x, dt, g, b, T, K, eps, q, s, y,
+                              _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "zq_ln_quant_fp8")
     return Xq, s_blk
@@ -404,12 +399,12 @@ def bias_act_quant_fp8(X: torch.Tensor, bias=None, act: int = ACT_NONE, Xq=None,
     """e4m3 quantization of token rows fused into a bias-add (act=ACT_NONE) or
     a bias-add and GeLU (act=ACT_GELU) (zq_bias_act_quant_fp8).  Returns as
     ln_quant_fp8; y, if given, receives the activation."""
-    dt, T, K = _matrix(X, "X")
-    e, dev = X.dtype, _current_device()
-    x, b = _ptr(X, e, (T, K), "X", dev), _ptr(bias, e, (K,), "bias", dev)
-    ya = _ptr(y, e, (T, K), "Y_act", dev)
-    Xq, s_blk, q, s = _fp8_out(X, T, K, T, Xq, s_blk, ("Xq", "s_blk"), dev)
-    rc = _lib.zq_bias_act_quant_fp8(x, dt, b, T, K, act, q, s, ya, _raw_stream(stream, dev))
+    x, dt, T, K, dev = _matrix(X, "X")
+    b = None if bias is None else _ptr(bias, X.dtype, (K,), "bias", dev)
+    ya = None if y is None else _ptr(y, X.dtype, (T, K), "Y_act", dev)
+    Xq, s_blk, q, s = _fp8_out(X, T, K, T, Xq, s_blk, dev)
+    rc = _lib.zq_bias_act_quant_fp8(x, dt, b, T, K, act, q, s, ya,
+                                    _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "zq_bias_act_quant_fp8")
     return Xq, s_blk
@@ -421,23 +416,24 @@ def gemm_fp8(Xq, s_x, Wq, s_w, bias=None, Y=None, out_dtype=torch.float16, strea
     dt = _DTYPES.get(out_dtype)
     if dt is None:
         raise TypeError(f"out_dtype must be torch.float16 or torch.bfloat16, got {out_dtype}")
-    for t, name in ((Xq, "Xq"), (Wq, "Wq")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dim() != 2:
-            raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    T, K = Xq.shape
-    N = Wq.shape[0]
+    if not (isinstance(Xq, torch.Tensor) and isinstance(Wq, torch.Tensor) and Xq.is_cuda):
+        raise TypeError("Xq and Wq must be CUDA tensors")
+    xs, ws = Xq.shape, Wq.shape
+    if len(xs) != 2 or len(ws) != 2:
+        raise ValueError(f"Xq and Wq must have two dimensions, got {tuple(xs)} and {tuple(ws)}")
+    T, K = xs
+    N = ws[0]
     kb, dev = -(-K // FP8_BLOCK), _current_device()
-    x, sx = _ptr(Xq, FP8, (T, K), "Xq", dev), _ptr(s_x, _F32, (T, kb), "s_x", dev)
-    w, sw = _ptr(Wq, FP8, (N, K), "Wq", dev), _ptr(s_w, _F32, (_blocks(N), kb), "s_w", dev)
-    b = _ptr(bias, out_dtype, (N,), "bias", dev)
+    x, sx = _ptr(Xq, FP8, xs, "Xq", dev), _ptr(s_x, _F32, (T, kb), "s_x", dev)
+    w, sw = _ptr(Wq, FP8, (N, K), "Wq", dev), _ptr(s_w, _F32, (-(-N // FP8_BLOCK), kb), "s_w", dev)
+    b = None if bias is None else _ptr(bias, out_dtype, (N,), "bias", dev)
     if Y is None:
-        Y = Xq.new_empty((T, N), dtype=out_dtype)
+        Y = torch.empty_strided((T, N), (N, 1), dtype=out_dtype, device=Xq.device)
         y = Y.data_ptr()
     else:
         y = _ptr(Y, out_dtype, (T, N), "Y", dev)
-    rc = _lib.zq_gemm_fp8(x, sx, w, sw, b, T, N, K, dt, y, _raw_stream(stream, dev))
+    rc = _lib.zq_gemm_fp8(x, sx, w, sw, b, T, N, K, dt, y,
+                          _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "zq_gemm_fp8")
     return Y
@@ -464,35 +460,35 @@ def rope_frequencies(R: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, f
     return torch.tensor(list(f), dtype=torch.float32), float(scale.value)
 
 
+def _strided(v, shape, dtype, what, dev):
+    """Strides and pointer of a [T, heads, D] tensor with contiguous heads."""
+    if not isinstance(v, torch.Tensor) or not v.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if v.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {v.dtype}")
+    if v.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(v.shape)}")
+    s = v.stride()
+    if s[2] != 1 and shape[2] > 1:
+        raise ValueError(f"the values of a head of {what} must be contiguous")
+    if v.get_device() != dev:
+        raise ValueError(f"{what} must be on the current device cuda:{dev}, got {v.device}")
+    # strides of dimensions of one element mean nothing and may be anything
+    return s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, v.data_ptr()
+
+
 def _heads(t, out, weight, bias, T, D, dtype, name, dev):
     """(zq_heads as bytes, out) of a strided [T, heads, D] tensor."""
-    H = t.shape[1] if isinstance(t, torch.Tensor) and t.dim() == 3 else -1
-    for what, v in ((name, t), (name + "_out", out)):
-        if v is None:
-            continue
-        if not isinstance(v, torch.Tensor) or not v.is_cuda:
-            raise TypeError(f"{what} must be a CUDA tensor")
-        if v.dtype is not dtype:
-            raise TypeError(f"{what} must be {dtype}, got {v.dtype}")
-        if v.shape != (T, H, D):
-            raise ValueError(f"{what} must have shape ({T}, {'heads' if H < 0 else H}, {D}), "
-                             f"got {tuple(v.shape)}")
-        if D > 1 and v.stride(2) != 1:
-            raise ValueError(f"the values of a head of {what} must be contiguous")
-        if v.get_device() != dev:
-            raise ValueError(f"{what} must be on the current device cuda:{dev}, got {v.device}")
+    if isinstance(t, torch.Tensor) and t.dim() != 3:
+        raise ValueError(f"{name} must have shape ({T}, heads, {D}), got {tuple(t.shape)}")
+    shape = (T, t.shape[1] if isinstance(t, torch.Tensor) else 0, D)
+    it, ih, i = _strided(t, shape, dtype, name, dev)
     if out is None:
-        out = torch.empty_like(t, memory_format=torch.contiguous_format)
-    # strides of dimensions of one element mean nothing and may be anything
-    a, b = t.stride(), out.stride()
-    it, ih, ot, oh = a[0], a[1], b[0], b[1]
-    if T <= 1:
-        it = ot = 0
-    if H <= 1:
-        ih = oh = 0
-    return _pack_heads(t.data_ptr(), out.data_ptr(),
-                       _ptr(weight, dtype, (D,), name + "_weight", dev) or 0,
-                       _ptr(bias, dtype, (D,), name + "_bias", dev) or 0, it, ih, ot, oh, H), out
+        out = torch.empty_like(t, memory_format=_CONTIGUOUS)
+    ot, oh, o = _strided(out, shape, dtype, name + "_out", dev)
+    w = 0 if weight is None else _ptr(weight, dtype, (D,), name + "_weight", dev)
+    b = 0 if bias is None else _ptr(bias, dtype, (D,), name + "_bias", dev)
+    return _pack_heads(i, o, w, b, it, ih, ot, oh, shape[1]), out
 
 
 def qk_norm_rope(q, k, positions, inv_freq, layout: int = ROPE_HALF, scale: float = 1.0,
@@ -526,7 +522,7 @@ def qk_norm_rope(q, k, positions, inv_freq, layout: int = ROPE_HALF, scale: floa
     if k is not None:
         hk, k_out = _heads(k, k_out, k_weight, k_bias, T, D, e, "k", dev)
     rc = _lib.zq_qk_norm_rope(hq, hk, dt, T, D, norm, eps, pos, f, 2 * half, layout, scale,
-                              _raw_stream(stream, dev))
+                              _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "zq_qk_norm_rope")
     return q_out, k_out
