@@ -108,6 +108,23 @@ __device__ __forceinline__ void widen8(const uint4& v, uint64_t (&y)[4]) {
   y[3] = widen2<E>(v.w);
 }
 
+// Largest magnitudes of two words of 16-bit values, half by half (NaN if any
+// is; magnitudes of 16-bit values need no widening to be compared).
+template <typename E>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w);
+template <>
+__device__ __forceinline__ uint32_t max_abs2<__half>(uint32_t m, uint32_t w) {
+  const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&m),
+                                __habs2(*reinterpret_cast<const __half2*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t max_abs2<__nv_bfloat16>(uint32_t m, uint32_t w) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // The factors that turn the values of one block into codes.  With
 // a = max(amax, 2^-110), the code of y is the e4m3 value nearest to
 // y * (448 / a).  448 / a is held as hi + lo (lo the remainder of the
