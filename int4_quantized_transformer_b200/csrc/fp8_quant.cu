@@ -32,15 +32,15 @@ __device__ __forceinline__ float quad_max(float v) {
 
 // Quantizes a lane's part of a block.  `col` is the block's first column, q
 // and y16 (may be null) its first value's place in the outputs.
-template <typename E>
+template <typename E, bool FULL = false>
 __device__ __forceinline__ void finish_block(const uint64_t (&y)[4 * kVecs], int lane, int col,
                                              int K, uint8_t* q, E* y16, float* s_out) {
   const BlockScale s = block_scale(quad_max(amax_pairs(y, 0.0f)));
-  if (lane == 0 && col < K) *s_out = s.scale;
+  if (lane == 0 && (FULL || col < K)) *s_out = s.scale;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int at = 8 * (lane + kLanes * i);
-    if (col + at < K) {
+    if (FULL || col + at < K) {
       *reinterpret_cast<uint2*>(q + at) = encode8(y + 4 * i, s);
       if (y16) *reinterpret_cast<uint4*>(y16 + at) = narrow8<E>(y + 4 * i);
     }
@@ -129,53 +129,69 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Sum over the `warps` warps of a row (the CTA); every thread gets it.  `red`
-// is written once between two uses of the other buffers.
-__device__ __forceinline__ float row_sum(float v, float* red, int warps) {
+// is written once between two uses of the other buffers; n is the power of two
+// from `warps` up.
+__device__ __forceinline__ float row_sum(float v, float* red, int warps, int n) {
   v = warp_sum(v);
   if (warps == 1) return v;
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  return warp_sum(lane < warps ? red[lane] : 0.0f);
+  const int at = threadIdx.x & (n - 1);
+  v = at < warps ? red[at] : 0.0f;
+  for (int o = n >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// 1 / sqrt(v) for v >= 0: the library's, corrected by a Newton step unless it
+// is 0 or infinite.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  const float c = __fmaf_rn(0.5f * r, __fmaf_rn(-v * r, r, 1.0f), r);
+  return r > 0.0f && r < INFINITY ? c : r;
 }
 
 // A warp has 1024 consecutive values of a row, 32 per lane; the row is read
 // once, its mean and then its centred sum of squares are taken over the
 // registers in fp32.  Rows of up to 1024 values: one per warp (ROWS = 4 to a
 // CTA), longer ones: one per CTA of at most THREADS.  The CTAs stay for many
-// rows; up to 512 threads the next row's loads are issued before the current
-// row is reduced (80 registers; with 64, for 32 warps per SM, they spill:
-// 29.0 instead of 21.7 us for 4096 x 6144, and 22.9 without them).  gamma and
-// beta come from L1.
-template <typename E, int ROWS, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS < 1024 ? 768 / THREADS : 1)
+// rows; with AHEAD the next row's loads are issued before the current row is
+// reduced, for which 80 registers have to be left to a thread.  FULL: no lane
+// of the CTA is past the row's end.  gamma and beta come from L1.
+// 4096 x 6144 in 19.6 us, 3.9 TB/s, bound by the latency of a row's two sums
+// and its block maxima at 24 warps per SM (issue slots 60% taken).  Without
+// AHEAD, at 32 warps, 20.5; the next row copied into shared memory instead of
+// registers 25.1; gamma and beta widened in shared memory 22.6; two rows at a
+// time 20.2; one barrier per row instead of two, by joining the warps' means
+// and squares, 19.9.
+template <typename E, int ROWS, int THREADS, int REGS, bool AHEAD, bool FULL>
+__global__ void __launch_bounds__(THREADS) __maxnreg__(REGS)
     fp8_ln_kernel(const E* __restrict__ X, const E* __restrict__ gamma, const E* __restrict__ beta,
                   int T, int K, float eps, uint8_t* __restrict__ Xq, float* __restrict__ s_blk,
                   E* __restrict__ Y) {
   __shared__ float red[2][2][32];
-  grid_dependency_wait();
-  grid_launch_dependents();
   const int warps = ROWS > 1 ? 1 : blockDim.x / 32;
   const int tid = ROWS > 1 ? (threadIdx.x & 31) : threadIdx.x;
+  int n = 1;  // the power of two from `warps` up
+  while (n < warps) n *= 2;
   const int lane = tid & (kLanes - 1), blk = tid / kLanes, col = blk * kFp8Block;
   const int kblocks = (K + kFp8Block - 1) / kFp8Block;
   const float inv_k = __fdiv_rn(1.0f, static_cast<float>(K));
   const uint4 zero = make_uint4(0, 0, 0, 0);
   auto offset = [&](int i) { return col + 8 * (lane + kLanes * i); };
+  auto in = [&](int i) { return FULL || offset(i) < K; };
   const long long stride = static_cast<long long>(gridDim.x) * ROWS;
   long long row = static_cast<long long>(blockIdx.x) * ROWS + (ROWS > 1 ? threadIdx.x / 32 : 0);
   uint4 x[kVecs];
   auto fetch = [&](long long r) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      x[i] = r < T && offset(i) < K
-                 ? __ldcs(reinterpret_cast<const uint4*>(X + r * K + offset(i)))
-                 : zero;
+      x[i] = r < T && in(i) ? __ldcs(reinterpret_cast<const uint4*>(X + r * K + offset(i))) : zero;
   };
-  constexpr bool kAhead = THREADS < 1024;
-  if (kAhead) fetch(row);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (AHEAD) fetch(row);
   for (int turn = 0; row < T; row += stride, turn ^= 1) {
-    if (!kAhead) fetch(row);
+    if (!AHEAD) fetch(row);
     uint64_t y[4 * kVecs];
     uint64_t sum2 = 0ull;
 #pragma unroll
@@ -187,14 +203,14 @@ __global__ void __launch_bounds__(THREADS, THREADS < 1024 ? 768 / THREADS : 1)
         sum2 = add_f32x2(sum2, y[4 * i + j]);
       }
     }
-    if (kAhead) fetch(row + stride);
+    if (AHEAD) fetch(row + stride);
     const float2 s2 = unpack_f32x2(sum2);
-    const float mean = row_sum(s2.x + s2.y, red[turn][0], warps) * inv_k;
+    const float mean = row_sum(s2.x + s2.y, red[turn][0], warps, n) * inv_k;
     const uint64_t minus = pack_f32x2(-mean, -mean);
     uint64_t sq2 = 0ull;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      if (offset(i) < K) {
+      if (in(i)) {
 #pragma unroll
         for (int j = 4 * i; j < 4 * i + 4; ++j) {
           y[j] = add_f32x2(y[j], minus);
@@ -203,36 +219,42 @@ __global__ void __launch_bounds__(THREADS, THREADS < 1024 ? 768 / THREADS : 1)
       }
     }
     const float2 q2 = unpack_f32x2(sq2);
-    const float var = row_sum(q2.x + q2.y, red[turn][1], warps) * inv_k;
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + eps));
+    const float rstd = inv_sqrt(row_sum(q2.x + q2.y, red[turn][1], warps, n) * inv_k + eps);
     const uint64_t rstd2 = pack_f32x2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      uint4 g = zero, b = zero;  // 0 past K
-      if (offset(i) < K) {
-        g = __ldg(reinterpret_cast<const uint4*>(gamma + offset(i)));
-        if (beta) b = __ldg(reinterpret_cast<const uint4*>(beta + offset(i)));
+      uint4 gv = zero, bv = zero;  // 0 past K
+      if (in(i)) {
+        gv = __ldg(reinterpret_cast<const uint4*>(gamma + offset(i)));
+        if (beta) bv = __ldg(reinterpret_cast<const uint4*>(beta + offset(i)));
       }
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, bw[4] = {b.x, b.y, b.z, b.w};
+      uint64_t g[4], b[4];
+      widen8<E>(gv, g);
+      widen8<E>(bv, b);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        y[4 * i + j] = fma_f32x2(mul_f32x2(y[4 * i + j], rstd2), widen2<E>(gw[j]), widen2<E>(bw[j]));
+        y[4 * i + j] = fma_f32x2(mul_f32x2(y[4 * i + j], rstd2), g[j], b[j]);
     }
     const size_t at = static_cast<size_t>(row) * K + col;
-    finish_block<E>(y, lane, col, K, Xq + at, Y ? Y + at : nullptr,
-                    s_blk + static_cast<size_t>(row) * kblocks + blk);
+    finish_block<E, FULL>(y, lane, col, K, Xq + at, Y ? Y + at : nullptr,
+                          s_blk + static_cast<size_t>(row) * kblocks + blk);
   }
 }
 
 template <typename E, int ROWS, int THREADS>
 cudaError_t launch_ln_one(int threads, const void* X, const void* gamma, const void* beta, int T,
                           int K, float eps, void* Xq, float* s_blk, void* Y, cudaStream_t st) {
-  const int ctas = (T - 1) / ROWS + 1;
-  const int per_sm = 65536 / ((THREADS < 1024 ? 80 : 64) * threads);  // by their registers
-  return launch_pdl(fp8_ln_kernel<E, ROWS, THREADS>, dim3(std::min(ctas, num_sms() * per_sm)),
-                    dim3(threads), 0, st, static_cast<const E*>(X), static_cast<const E*>(gamma),
-                    static_cast<const E*>(beta), T, K, eps, static_cast<uint8_t*>(Xq), s_blk,
-                    static_cast<E*>(Y));
+  constexpr bool kAhead = THREADS <= 768;
+  constexpr int kRegs = kAhead ? 80 : 64;
+  const int ctas = (T - 1) / ROWS + 1, per_sm = 65536 / (kRegs * threads);
+  auto go = [&](auto* kernel) {
+    return launch_pdl(kernel, dim3(std::min(ctas, num_sms() * per_sm)), dim3(threads), 0, st,
+                      static_cast<const E*>(X), static_cast<const E*>(gamma),
+                      static_cast<const E*>(beta), T, K, eps, static_cast<uint8_t*>(Xq), s_blk,
+                      static_cast<E*>(Y));
+  };
+  return K % 1024 == 0 ? go(fp8_ln_kernel<E, ROWS, THREADS, kRegs, kAhead, true>)
+                       : go(fp8_ln_kernel<E, ROWS, THREADS, kRegs, kAhead, false>);
 }
 
 template <typename E>
@@ -240,10 +262,8 @@ cudaError_t launch_ln(const void* X, const void* gamma, const void* beta, int T,
                       void* Xq, float* s_blk, void* Y, cudaStream_t st) {
   const int warps = (K + 1023) / 1024;
   if (warps == 1) return launch_ln_one<E, 4, 128>(128, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-  if (warps <= 8)
-    return launch_ln_one<E, 1, 256>(32 * warps, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
-  if (warps <= 16)
-    return launch_ln_one<E, 1, 512>(32 * warps, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
+  if (warps <= 24)  // 768 threads of 80 registers still fit
+    return launch_ln_one<E, 1, 768>(32 * warps, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
   return launch_ln_one<E, 1, 1024>(32 * warps, X, gamma, beta, T, K, eps, Xq, s_blk, Y, st);
 }
 
