@@ -20,8 +20,9 @@
 namespace zq {
 namespace {
 
-constexpr int kThreads = 256;  // of a CTA without a norm, and with one
-constexpr int kNormThreads = 64;
+constexpr int kThreads = 256;  // of a CTA without a norm
+constexpr int kNormWarps = 12;  // most of a CTA with one
+constexpr int kSmNormWarps = 24;  // of an SM: 80 registers per thread
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxTokens = 16;    // of a CTA
 constexpr int kMaxAngles = 1024;  // sines (and cosines) of a CTA, padded
@@ -265,7 +266,8 @@ struct NormCut {
 };
 
 template <typename E, int CUT>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const RopeParams p, int lanes) {
+__global__ void __launch_bounds__(32 * kNormWarps, kSmNormWarps / kNormWarps)
+    norm_rope_kernel(const RopeParams p, int lanes) {
   using C = NormCut<CUT>;
   constexpr bool HALF = CutOf<CUT>::HALF;
   constexpr int NU = C::NU, VEC = C::VEC, TAIL = C::TAIL, WIDE = C::WIDE;
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const RopeParam
   grid_launch_dependents();
   const Tile tl = tile_of(p);
   const int lane = threadIdx.x & (lanes - 1);
-  int head = (tl.column * kNormThreads + static_cast<int>(threadIdx.x)) / lanes;
+  int head = (tl.column * blockDim.x + static_cast<int>(threadIdx.x)) / lanes;
   // lanes past the last head go along for the group sums, with nothing to read
   const bool live = head < p.set[0].n + p.set[1].n;
   const int which = live && head >= p.set[0].n;
@@ -415,6 +417,27 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const RopeParam
   }
 }
 
+// Warps of a CTA with a norm, for heads that take `total` warps per token.
+// Each column of CTAs computes the tokens' sines again, which costs a thread
+// about as much per angle as 1/58 of a token; and columns that leave warps
+// idle, or do not fill an SM's 24, cost in proportion.  Measured against 64
+// threads for all: 2011 tokens of 40 heads of 128 (10 warps) in 11.1 us (13.0),
+// 16384 of them in 68.5 (78.9), 8192 tokens of 20 heads of 256 in 35.4 (38.7).
+// For 4096 tokens of 128 heads of 96, LayerNorm (32 warps; takes 8) 61.2 us,
+// 11 warps 73, 2 warps 63.
+int norm_warps(long long T, long long total, int row) {
+  if (T * total <= 4ll * num_sms()) return 2;  // a few tokens: over the SMs
+  int best = 1;
+  double best_rate = 0.0;
+  for (int w = 1; w <= kNormWarps; ++w) {
+    const long long columns = (total + w - 1) / w;
+    const double useful = static_cast<double>(total) / (columns * w) * (kSmNormWarps / w * w);
+    const double rate = useful / (1.0 + row * (1.0 / 58) / w);
+    if (rate >= best_rate) best = w, best_rate = rate;
+  }
+  return best;
+}
+
 template <typename E, int CUT, bool NORM>
 cudaError_t launch_cut(const RopeParams& p0, cudaStream_t st) {
   using C = CutOf<CUT>;
@@ -425,17 +448,24 @@ cudaError_t launch_cut(const RopeParams& p0, cudaStream_t st) {
   const long long threads =
       NORM ? heads * lanes
            : heads * (C::rotated_units(p.R) + (p.copy_rest ? C::tail_units(p.D, p.R) : 0));
-  constexpr int cta = NORM ? kNormThreads : kThreads;
+  // tokens of a CTA at most: their sines have to fit
+  const int row = std::max(4, (p.R / 2 + 3) & ~3), most = std::min(kMaxTokens, kMaxAngles / row);
+  const int cta = NORM ? 32 * norm_warps(p.T, (threads + 31) / 32, row) : kThreads;
   const long long columns = (threads + cta - 1) / cta;
-  // As many tokens to a CTA as leave so many CTAs for each SM (their sines
-  // have to fit).  Measured: 4096 tokens of 2 x 64 heads of 96 values, no norm,
-  // 4, 16 and 24 per SM: 46.8, 40.9 and 37.2 us, but 8192 tokens of 2 x 16
-  // heads of 80 best with 16 (19.5 us); with a norm, 2011 tokens of 40 heads
-  // of 128 in CTAs of 256, 128 and 64 threads: 17.7, 13.3 and 12.9 us.
-  const int row = std::max(4, (p.R / 2 + 3) & ~3);
-  const long long want = (NORM ? 16ll : 20ll) * num_sms();
-  p.tokens = static_cast<int>(
-      std::max(1ll, std::min<long long>(p.T * columns / want, std::min(kMaxTokens, kMaxAngles / row))));
+  if (NORM) {
+    // whole waves of CTAs, the tokens spread over them evenly
+    const long long tiles =
+        std::max(1ll, static_cast<long long>(kSmNormWarps * 32 / cta) * num_sms() / columns);
+    const long long waves = (p.T - 1) / (tiles * most) + 1;
+    p.tokens = static_cast<int>((p.T - 1) / (waves * tiles) + 1);
+  } else {
+    // As many tokens as leave 20 CTAs for each SM.  Measured: 4096 tokens of
+    // 2 x 64 heads of 96 values, 4, 16 and 24 per SM: 46.8, 40.9 and 37.2 us,
+    // but 8192 tokens of 2 x 16 heads of 80 best with 16 (19.5 us); whole
+    // waves as above 42.6 to 45.4 and 19.2 us.
+    const long long want = 20ll * num_sms();
+    p.tokens = static_cast<int>(std::max(1ll, std::min<long long>(p.T * columns / want, most)));
+  }
   const long long ctas = (static_cast<long long>(p.T) + p.tokens - 1) / p.tokens * columns;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
   p.columns = static_cast<int>(columns);
