@@ -164,7 +164,7 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 // time 20.2; one barrier per row instead of two, by joining the warps' means
 // and squares, 19.9.
 template <typename E, int ROWS, int THREADS, int REGS, bool AHEAD, bool FULL>
-__global__ void __launch_bounds__(THREADS) __maxnreg__(REGS)
+__global__ void __launch_bounds__(THREADS, 65536 / (REGS * THREADS))
     fp8_ln_kernel(const E* __restrict__ X, const E* __restrict__ gamma, const E* __restrict__ beta,
                   int T, int K, float eps, uint8_t* __restrict__ Xq, float* __restrict__ s_blk,
                   E* __restrict__ Y) {
@@ -246,7 +246,8 @@ cudaError_t launch_ln_one(int threads, const void* X, const void* gamma, const v
                           int K, float eps, void* Xq, float* s_blk, void* Y, cudaStream_t st) {
   constexpr bool kAhead = THREADS <= 768;
   constexpr int kRegs = kAhead ? 80 : 64;
-  const int ctas = (T - 1) / ROWS + 1, per_sm = 65536 / (kRegs * threads);
+  // CTAs of an SM: 6 warps of 80 registers, or 8 of 64, fit each of its four schedulers
+  const int ctas = (T - 1) / ROWS + 1, per_sm = (kAhead ? 24 : 32) * 32 / threads;
   auto go = [&](auto* kernel) {
     return launch_pdl(kernel, dim3(std::min(ctas, num_sms() * per_sm)), dim3(threads), 0, st,
                       static_cast<const E*>(X), static_cast<const E*>(gamma),

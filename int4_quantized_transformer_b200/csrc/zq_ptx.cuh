@@ -99,27 +99,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// As mbar_wait for waits on a kernel's critical path: the thread lets the
-// hardware suspend it for up to 20 us per try (polling a barrier takes shared
-// memory cycles from the copies and the MMAs) and looks at the timer only
-// when many tries have failed.
-__device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                              int* status, int where) {
-#pragma unroll 1
-  for (int it = 0; it < 64; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
-  }
-  return mbar_wait(bar, parity, abort, status, where);
-}
-
 // ------------------------------------------------- programmatic dependent launch
 // Block until every grid this one depends on (the previous kernel in the
 // stream, when launched with programmatic stream serialization) has finished
