@@ -63,7 +63,7 @@ cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& ready) {
 
 // ------------------------------------------------------------ weight rows
 //
-// Up to 128 tokens: the weights' bytes bound the call, so they have to flow
+// Up to 64 tokens: the weights' bytes bound the call, so they have to flow
 // without a pause.  A CTA has R weight rows (the 128-row operand of its
 // MMAs; rows past R are never looked at) and TN token
 // columns, streamed through a deep ring of 128-k slices by TMA.  The MMAs of
@@ -84,8 +84,10 @@ constexpr int kRowsAccWarps = 8;
 constexpr int kRowsThreads = 32 * (4 + kRowsAccWarps);  // copies, MMAs, scales (two warps)
 constexpr int kRowsMaxStages = 16;
 // Two CTAs fit an SM: their waits and ends overlap, and the next call's
-// set-up and first copies to L2 overlap the end of this one.
-constexpr int kRowsSmem = 112 * 1024;
+// set-up and first copies to L2 overlap the end of this one.  A third must not
+// fit: two have all of tensor memory, and CTAs of a cluster that wait for one
+// another must not wait for its allocation in a circle.
+constexpr int kRowsSmem = 112 * 1024, kRowsMinSmem = 77 * 1024;
 
 template <int TN_>
 struct RowsCfg {
@@ -411,7 +413,7 @@ cudaError_t launch_rows_gemm(const Fp8Params& p, int rows, int split, cudaStream
                        (p.kblocks + split - 1) / split);
   rp.off_slots = (rp.stages * rp.stage_bytes + over + 15) / 16 * 16;
   rp.off_xchg = rp.off_slots + (slots + 15) / 16 * 16;
-  const int smem = rp.off_xchg + xchg + 1024;
+  const int smem = std::max(rp.off_xchg + xchg + 1024, kRowsMinSmem);
   CUtensorMap mx, mw;
   if (!encode_tma_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.Xq, p.K, p.T, p.K, kFp8Block, C::TN,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(32 * kNormWarps, kSmNormWarps / kNormWarps)
 // 16384 of them in 68.5 (78.9), 8192 tokens of 20 heads of 256 in 35.4 (38.7).
 // For 4096 tokens of 128 heads of 96, LayerNorm (32 warps; takes 8) 61.2 us,
 // 11 warps 73, 2 warps 63.
-int norm_warps(long long T, long long total, int row) {
-  if (T * total <= 4ll * num_sms()) return 2;  // a few tokens: over the SMs
+long long norm_warps(long long T, long long total, int row) {
+  if (T * total <= 4ll * num_sms()) return std::min(2ll, total);  // a few tokens: over the SMs
   int best = 1;
   double best_rate = 0.0;
   for (int w = 1; w <= kNormWarps; ++w) {
@@ -450,7 +450,7 @@ cudaError_t launch_cut(const RopeParams& p0, cudaStream_t st) {
            : heads * (C::rotated_units(p.R) + (p.copy_rest ? C::tail_units(p.D, p.R) : 0));
   // tokens of a CTA at most: their sines have to fit
   const int row = std::max(4, (p.R / 2 + 3) & ~3), most = std::min(kMaxTokens, kMaxAngles / row);
-  const int cta = NORM ? 32 * norm_warps(p.T, (threads + 31) / 32, row) : kThreads;
+  const int cta = NORM ? static_cast<int>(32 * norm_warps(p.T, (threads + 31) / 32, row)) : kThreads;
   const long long columns = (threads + cta - 1) / cta;
   if (NORM) {
     // whole waves of CTAs, the tokens spread over them evenly

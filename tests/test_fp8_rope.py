@@ -20,6 +20,9 @@ Tolerances (u = 2^-24, half a step of fp32; half steps of the 16-bit types
   step of the output type.
 """
 import math
+import os
+import subprocess
+import sys
 import unittest.mock as mock
 
 import numpy as np
@@ -594,6 +597,116 @@ def test_layer_together(zq, T):
     rel = float((y.cpu().double() - ry).norm() / ry.norm())
     assert rel <= 4 * 2 * 2.0 ** -4, rel
     assert rel > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [16, 272, 1024, 1040, 2048, 5120, 6160, 12288, 16400, 24576, 24592, 32768])
+def test_layernorm_rows_do_not_depend_on_their_number(zq, K):
+    """More rows than run at once, and each row's bits as in a call of its own
+    few."""
+    T = 148 * 24 * 4 // (1 if K <= 1024 else 4 * -(-K // 1024)) * 2 + 5
+    x = torch.randn(T, K, generator=gen(K)).half().cuda()
+    gamma = (1 + 0.1 * torch.randn(K, generator=gen(K + 1))).half().cuda()
+    y = torch.empty_like(x)
+    q, s = zq.ln_quant_fp8(x, gamma, gamma, y_ln=y)
+    for a, b in ((0, 1), (1, 40), (T // 2, T // 2 + 9), (T - 7, T)):
+        yc = torch.empty_like(x[a:b])
+        qc, sc = zq.ln_quant_fp8(x[a:b], gamma, gamma, y_ln=yc)
+        assert torch.equal(q[a:b].view(torch.uint8), qc.view(torch.uint8))
+        assert torch.equal(s[a:b], sc) and torch.equal(y[a:b], yc)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", [0, 1, 2])
+@pytest.mark.parametrize("T,Hq,Hk,D,R,layout", [(6001, 2, 1, 64, 64, 0), (2011, 32, 8, 128, 128, 0),
+                                                (700, 64, 64, 96, 24, 0), (3000, 16, 4, 256, 64, 1)])
+def test_rope_tokens_do_not_depend_on_their_number(zq, norm, T, Hq, Hk, D, R, layout):
+    g = gen(T)
+    q, k = torch.randn(T, Hq, D, generator=g).half().cuda(), torch.randn(T, Hk, D, generator=g).half().cuda()
+    pos = torch.randint(0, 100000, (T,), generator=g).int().cuda()
+    f = zq.rope_frequencies(R)[0].cuda()
+    qo, ko = zq.qk_norm_rope(q, k, pos, f, layout, norm=norm)
+    for a, b in ((0, 1), (1, 30), (T // 2, T // 2 + 5), (T - 3, T)):
+        qc, kc = zq.qk_norm_rope(q[a:b], k[a:b], pos[a:b], f, layout, norm=norm)
+        assert torch.equal(qo[a:b], qc) and torch.equal(ko[a:b], kc)
+
+
+@pytest.mark.gpu
+def test_kernels_with_tensor_memory_side_by_side(zq):
+    """FP8 GEMMs of few tokens (clusters along K), of some (clusters of tiles)
+    and of many (CTA pairs), and the INT8 GEMM's pairs, on four streams at
+    once: each gives what it gives alone."""
+    g = gen(3)
+    jobs = []
+    for T, K, N in ((8, 4096, 1024), (200, 4096, 512), (2048, 2048, 2048)):
+        x = quantized(zq, torch.randn(T, K, generator=g), 1, 0)
+        w = quantized(zq, torch.randn(N, K, generator=g), 128, 0)
+        jobs.append(lambda x=x, w=w: zq.gemm_fp8(*x, *w))
+    X = torch.randn(2048, 2048, generator=g).half().cuda()
+    Wq, sg = zq.quantize_weights_groupwise(torch.randn(2048, 2048, generator=g).half().cuda(), 16, 8)
+    Xq, st = zq.ln_quant(X)
+    Y8 = torch.empty(2048, 2048, dtype=torch.float16, device="cuda")
+    jobs.append(lambda: zq.gemm_w8a8(Xq, st, Wq, sg, Y=Y8))
+    want = [job().clone() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(30):
+        for job, s, out in zip(jobs, streams, got):
+            with torch.cuda.stream(s):
+                out.append(job())
+    torch.cuda.synchronize()
+    for w, out in zip(want, got):
+        assert all(torch.equal(w, y) for y in out)
+
+
+_FIRST_CALLS_IN_A_CAPTURE = r"""
+import sys, torch
+sys.path.insert(0, {root!r})
+from int4_quantized_transformer_b200 import zq
+g = torch.Generator().manual_seed(1)
+K, N = 2048, 1024
+W = torch.randn(N, K, generator=g).half().cuda()
+xs = [torch.randn(T, K, generator=g).half().cuda() for T in (1, 40, 200, 1500)]
+gamma = torch.ones(K, dtype=torch.float16, device="cuda")
+pos = torch.arange(1500, dtype=torch.int32, device="cuda")
+f = zq.rope_frequencies(64)[0].cuda()
+# the library's own CUDA runtime starts up at its first call: make that call
+# (a status query) outside any capture
+assert zq.device_status()[0] == zq.ZQ_OK
+
+def run():
+    w = zq.quantize_weights_fp8(W)
+    out = []
+    for x in xs:
+        T = x.shape[0]
+        y = zq.gemm_fp8(*zq.ln_quant_fp8(x, gamma), *w)
+        out += [y, zq.gemm_fp8(*zq.bias_act_quant_fp8(x, None, zq.ACT_GELU), *w)]
+        out += zq.qk_norm_rope(y.view(T, 16, 64)[:, :12], y.view(T, 16, 64)[:, 12:], pos[:T], f,
+                               norm=zq.NORM_RMS)
+        out += zq.qk_norm_rope(y.view(T, 16, 64)[:, :12], y.view(T, 16, 64)[:, 12:], pos[:T], f)
+    return out
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+for _ in range(2):
+    graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(got, run()):
+    assert torch.equal(a, b)
+assert zq.device_status()[0] == zq.ZQ_OK
+print("ok")
+"""
+
+
+@pytest.mark.gpu
+def test_first_calls_in_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", _FIRST_CALLS_IN_A_CAPTURE.format(root=root)],
+                         capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-3000:]
+    assert out.stdout.split()[-1] == "ok"
 
 
 # ------------------------------------------------------------ frequencies (host)
