@@ -287,9 +287,9 @@ typedef enum { ZQ_F16 = 0, ZQ_BF16 = 1 } zq_dtype;
  * Quantization of one block, shared by the calls below: with amax the largest
  * magnitude in the block (of fp32 values) and a = max(amax, 2^-110),
  *   scale = a / 448,   code = e4m3(y * (448 / a)),
- * the division rounded once, the code rounded to nearest even from a product
- * whose relative error is at most 2^-24 and which is exact where the quotient
- * lies exactly between two codes.  An all-zero block has scale 0 and codes 0.
+ * the scale within one unit of 2^-24 of the exact quotient, the code rounded
+ * to nearest even from a product whose relative error is at most 2^-24 and
+ * which is exact where the quotient lies exactly between two codes.  An all-zero block has scale 0 and codes 0.
  * A block with Inf or NaN in it has scale Inf or NaN and NaN codes, so that
  * it shows in every output that it reaches.
  *
@@ -349,8 +349,14 @@ zq_status zq_bias_act_quant_fp8(const void* X, int dtype, const void* bias, int 
  * overlap.
  * Requirements: T >= 0 (T == 0 is a no-op), N >= 8, N % 8 == 0,
  * 16 <= K <= 2^20, K % 16 == 0, pointers 16-byte aligned (scales 4-byte).
- * ZQ_OPT_GEMM_PATH forces a kernel: 1 = the tensor-memory tiles, 2 = weight
- * streaming (other values: ZQ_ERR_UNSUPPORTED).
+ * Up to 64 tokens the weight rows are the 128-row side of the MMAs and a ring
+ * of TMA copies streams them; above, tiles of 128 token rows (or CTA pairs of
+ * 256) by 128 or 256 weight rows.  Options (other values than these:
+ * ZQ_ERR_UNSUPPORTED): ZQ_OPT_GEMM_PATH 1 = tiles, 2 = weight rows (T <= 64);
+ * ZQ_OPT_SPLIT_K 1 to 8, at most KB: that many CTAs of a cluster share a tile
+ * (or rows) along K; ZQ_OPT_GEMM_BN 128 or 256 and ZQ_OPT_CTA_PAIR as for
+ * zq_gemm_w8a8: the tiles' width and pairs; ZQ_OPT_MAX_CTAS: CTAs of the
+ * weight-row kernel.
  */
 zq_status zq_gemm_fp8(const void* Xq, const float* s_x, const void* Wq, const float* s_w,
                       const void* bias, int T, int N, int K, int dtype, void* Y,
