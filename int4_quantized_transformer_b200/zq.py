@@ -311,11 +311,15 @@ def gemm_w4a16(X, Wq4, s_grp, bias=None, Y=None, acc_dbg=None, stream=None):
 FP8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # zq_dtype
-_F32, _I32, _CONTIGUOUS = torch.float32, torch.int32, torch.contiguous_format
+_F32, _I32 = torch.float32, torch.int32
 # the plain getters behind torch.cuda.current_device() and current_stream()
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+# (shape, strides, dtype) -> a new tensor on the current device: torch's own
+# short way there where it has one (0.8 us instead of 1.7)
+_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None) \
+    or (lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda"))
 
 
 def _ptr(t, dtype, shape, name: str, dev: int):
@@ -346,16 +350,16 @@ def _matrix(t, name: str):
     return t.data_ptr(), d, shape[0], shape[1], dev
 
 
-def _fp8_out(X, rows, cols, scale_rows, Xq, s_blk, dev):
+def _fp8_out(rows, cols, scale_rows, Xq, s_blk, dev):
     """Codes and scales (made where not given) and their pointers."""
     kb = -(-cols // FP8_BLOCK)
     if Xq is None:
-        Xq = torch.empty_like(X, dtype=FP8, memory_format=_CONTIGUOUS)
+        Xq = _new((rows, cols), (cols, 1), FP8)
         q = Xq.data_ptr()
     else:
         q = _ptr(Xq, FP8, (rows, cols), "Xq" if rows == scale_rows else "Wq", dev)
     if s_blk is None:
-        s_blk = torch.empty_strided((scale_rows, kb), (kb, 1), dtype=_F32, device=X.device)
+        s_blk = _new((scale_rows, kb), (kb, 1), _F32)
         s = s_blk.data_ptr()
     else:
         s = _ptr(s_blk, _F32, (scale_rows, kb), "s_blk", dev)
@@ -367,7 +371,7 @@ def quantize_weights_fp8(W: torch.Tensor, Wq=None, s_blk=None, stream=None):
     block (zq_quantize_weights_fp8).  Returns (Wq float8_e4m3fn [N,K],
     s_blk fp32 [ceil(N/128), ceil(K/128)])."""
     w, dt, N, K, dev = _matrix(W, "W")
-    Wq, s_blk, q, s = _fp8_out(W, N, K, -(-N // FP8_BLOCK), Wq, s_blk, dev)
+    Wq, s_blk, q, s = _fp8_out(N, K, -(-N // FP8_BLOCK), Wq, s_blk, dev)
     rc = _lib.zq_quantize_weights_fp8(
         w, dt, N, K, q, s, _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
@@ -386,7 +390,7 @@ def ln_quant_fp8(X: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, Xq=N
     g = None if gamma is None else _ptr(gamma, e, (K,), "gamma", dev)
     b = None if beta is None else _ptr(beta, e, (K,), "beta", dev)
     y = None if y_ln is None else _ptr(y_ln, e, (T, K), "Y_ln", dev)
-    Xq, s_blk, q, s = _fp8_out(X, T, K, T, Xq, s_blk, dev)
+    Xq, s_blk, q, s = _fp8_out(T, K, T, Xq, s_blk, dev)
     rc = _lib.zq_ln_quant_fp8(x, dt, g, b, T, K, eps, q, s, y,
                               _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
@@ -402,7 +406,7 @@ def bias_act_quant_fp8(X: torch.Tensor, bias=None, act: int = ACT_NONE, Xq=None,
     x, dt, T, K, dev = _matrix(X, "X")
     b = None if bias is None else _ptr(bias, X.dtype, (K,), "bias", dev)
     ya = None if y is None else _ptr(y, X.dtype, (T, K), "Y_act", dev)
-    Xq, s_blk, q, s = _fp8_out(X, T, K, T, Xq, s_blk, dev)
+    Xq, s_blk, q, s = _fp8_out(T, K, T, Xq, s_blk, dev)
     rc = _lib.zq_bias_act_quant_fp8(x, dt, b, T, K, act, q, s, ya,
                                     _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
@@ -428,7 +432,7 @@ def gemm_fp8(Xq, s_x, Wq, s_w, bias=None, Y=None, out_dtype=torch.float16, strea
     w, sw = _ptr(Wq, FP8, (N, K), "Wq", dev), _ptr(s_w, _F32, (-(-N // FP8_BLOCK), kb), "s_w", dev)
     b = None if bias is None else _ptr(bias, out_dtype, (N,), "bias", dev)
     if Y is None:
-        Y = torch.empty_strided((T, N), (N, 1), dtype=out_dtype, device=Xq.device)
+        Y = _new((T, N), (N, 1), out_dtype)
         y = Y.data_ptr()
     else:
         y = _ptr(Y, out_dtype, (T, N), "Y", dev)
@@ -461,34 +465,41 @@ def rope_frequencies(R: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, f
 
 
 def _strided(v, shape, dtype, what, dev):
-    """Strides and pointer of a [T, heads, D] tensor with contiguous heads."""
+    """Token and head stride and pointer of a [T, heads, D] tensor with
+    contiguous heads."""
     if not isinstance(v, torch.Tensor) or not v.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
     if v.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {v.dtype}")
     if v.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(v.shape)}")
-    s = v.stride()
-    if s[2] != 1 and shape[2] > 1:
+    token, head, value = v.stride()
+    if value != 1 and shape[2] > 1:
         raise ValueError(f"the values of a head of {what} must be contiguous")
     if v.get_device() != dev:
         raise ValueError(f"{what} must be on the current device cuda:{dev}, got {v.device}")
     # strides of dimensions of one element mean nothing and may be anything
-    return s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, v.data_ptr()
+    return token if shape[0] > 1 else 0, head if shape[1] > 1 else 0, v.data_ptr()
 
 
 def _heads(t, out, weight, bias, T, D, dtype, name, dev):
     """(zq_heads as bytes, out) of a strided [T, heads, D] tensor."""
-    if isinstance(t, torch.Tensor) and t.dim() != 3:
-        raise ValueError(f"{name} must have shape ({T}, heads, {D}), got {tuple(t.shape)}")
-    shape = (T, t.shape[1] if isinstance(t, torch.Tensor) else 0, D)
+    heads = 0
+    if isinstance(t, torch.Tensor):
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have shape ({T}, heads, {D}), got {tuple(t.shape)}")
+        heads = t.shape[1]
+    shape = (T, heads, D)
     it, ih, i = _strided(t, shape, dtype, name, dev)
     if out is None:
-        out = torch.empty_like(t, memory_format=_CONTIGUOUS)
-    ot, oh, o = _strided(out, shape, dtype, name + "_out", dev)
+        ot, oh = heads * D, D
+        out = _new(shape, (ot, oh, 1), dtype)
+        o = out.data_ptr()
+    else:
+        ot, oh, o = _strided(out, shape, dtype, name + "_out", dev)
     w = 0 if weight is None else _ptr(weight, dtype, (D,), name + "_weight", dev)
     b = 0 if bias is None else _ptr(bias, dtype, (D,), name + "_bias", dev)
-    return _pack_heads(i, o, w, b, it, ih, ot, oh, shape[1]), out
+    return _pack_heads(i, o, w, b, it, ih, ot, oh, heads), out
 
 
 def qk_norm_rope(q, k, positions, inv_freq, layout: int = ROPE_HALF, scale: float = 1.0,
