@@ -842,7 +842,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float fx, fw;
       factor_at(0, fx, fw);
       // The loads from tensor memory never pause: while a chunk of columns is
-      // added the next one is on its way, across blocks too.
+      // added the next one is on its way, across blocks too.  (A wait that gave
+      // up ends the tile behind its last block; the waits until then give up at
+      // once.  With an exit from the loop the sums took 1.3% longer.)
       static_assert(COLS / kChunk % 2 == 0, "the chunk buffers alternate across blocks");
       uint32_t r[2][kChunk];
       if (!wait_all(&tfull_bar[buf * HALVES + half], tphase, abort_flag, p.status, 36)) break;
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tphase = next_phase;
             if (more) {
               if (!__all_sync(0xffffffffu, probe))
-                ok = wait_all(&tfull_bar[buf * HALVES + half], tphase, abort_flag, p.status, 36);
+                ok &= wait_all(&tfull_bar[buf * HALVES + half], tphase, abort_flag, p.status, 36);
               tc_fence_after();
               tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(buf * C::BN), r[0]);
             }
@@ -890,7 +892,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               if (lane == 0) mbar_arrive(&sempty_bar[slot]);
               slot ^= 1;
               sphase ^= slot == 0;
-              ok = next_group();
+              ok &= next_group();
             }
             factor_at(j, fx, fw);
           }
@@ -898,11 +900,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int i = 0; i < kChunk / 2; ++i)
             fma_f32x2(acc[kChunk / 2 * c + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], s2);
         }
-        if (!ok) {
-          tmem_ld_wait();
-          break;
-        }
       }
+      tmem_ld_wait();
       if (!ok) break;
       if constexpr (!C::SPLIT) {
         // Bias, rounding, and 32 bytes of a row per store: whole sectors, and
