@@ -463,13 +463,16 @@ cudaError_t launch_rows_any(const Fp8Params& p, cudaStream_t st) {
 // block, so the factor is one number per lane and stage.
 //
 // 4096 x 6144 x 18432 takes 419 us alone (2.2 PFLOP/s) and 490 to 505 in a row,
-// where power lowers the clock.  The tensor pipe is busy 55% of that: a block
-// is 512 cycles of MMAs for a pair of 256 x 256, but each scheduler brings 32
-// KB of sums from tensor memory and adds them in about 950 (a 4 KB load holds
-// the issue for 52 to 90 cycles, its FMAs for 32).  Three to six stages, 16
-// accumulating warps, loads of 16 columns and two blocks per accumulator
-// buffer all measured the same or slower; single CTAs of 128 x 256 are 7%
-// slower, tiles of 128 columns 40% and more.
+// where power lowers the clock: 636 thousand cycles, of which the MMAs alone
+// are 383.  With parts left out (and the results wrong): without the FMAs 543,
+// without the output's stores 617, without both 470, without the scales' copies
+// too 413.  A block's sums wait for their MMAs, are loaded, added, and handed
+// back across the pair, with two buffers to cover that: the FMAs (256 cycles per
+// block and scheduler at best, 512 the MMAs) lengthen it, the loads from tensor
+// memory do not.  Three to six stages, 12 or 16 accumulating warps (192 columns
+// or 16-column loads), 256-column MMAs, releasing a buffer earlier and one look
+// at all barriers at once measured the same or slower; single CTAs of 128 x 256
+// are 7% slower, tiles of 128 columns 40% and more.
 //
 // With too few tiles for the SMs, the CTAs of a cluster share a tile, each
 // with its own part of the blocks; they exchange their partial sums through
@@ -488,13 +491,6 @@ constexpr int kTileThreads = 32 * (kAccWarp0 + kAccWarps);
 // what the first four warps give: 4 * 56 + 8 * 224 = 12 * 168.
 constexpr int kRegsFirst = 56, kRegsAcc = 224;
 constexpr int kTileSmem = 226 * 1024;
-// Scales travel in groups of eight blocks, [block][token row] with four words
-// of padding (so that a warp that reads rows of eight scales writes each to
-// another bank), followed by the weight scales of the tile's weight blocks.
-constexpr int kGroup = 8;
-constexpr int kGroupRow = BM + 4;
-constexpr int kGroupBytes = (kGroup * kGroupRow + 2 * kGroup) * 4;
-
 template <int BN_, bool PAIR_, bool SPLIT_>
 struct TileCfg {
   static constexpr int BN = BN_;
@@ -520,17 +516,28 @@ struct TileCfg {
   static constexpr int PIECES = COLS / 4;
   static constexpr int XCHG_BYTES = SPLIT ? 21 * 32 * kAccWarps * 16 : 0;
   static_assert(!SPLIT || PIECES == 16, "room for the partial sums");
-  static constexpr int AUX_BYTES = 2 * kGroupBytes + 2 * BN * 2;  // two scale groups, two units' bias
+  // Scales travel in groups of blocks, [block][token row] (padded, so that a
+  // warp that copies rows of scales writes each to another bank), followed by
+  // the weight scales of the tile's two weight blocks: 32 blocks, a line of
+  // 128 bytes of each row's (in groups of eight, 32 bytes of a row, their
+  // requests to L2 held up the copies: tiles of 256 x 128 took 12% longer), and
+  // eight where a CTA has a part of the blocks only.
+  static constexpr int GROUP = SPLIT ? 8 : 32;
+  static constexpr int GROUP_ROW = SPLIT ? BM + 4 : BM + 1;
+  static constexpr int GROUP_BYTES = (GROUP * GROUP_ROW + 2 * GROUP) * 4;
+  static constexpr int SLOTS = 2;  // groups on their way or in use
+  // and the bias of as many units (one can take a single group)
+  static constexpr int AUX_BYTES = SLOTS * (GROUP_BYTES + BN * 2);
   static constexpr int STAGES_RAW =
       (kTileSmem - 1536 - XCHG_BYTES - AUX_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
   static_assert(STAGES >= 3, "pipeline depth");
   static constexpr int OFF_XCHG = STAGES * STAGE_BYTES;
   static constexpr int OFF_AUX = OFF_XCHG + XCHG_BYTES;
-  static constexpr int OFF_BIAS = OFF_AUX + 2 * kGroupBytes;
+  static constexpr int OFF_BIAS = OFF_AUX + SLOTS * GROUP_BYTES;
   static constexpr int OFF_BAR = OFF_AUX + AUX_BYTES;
   static_assert(OFF_BIAS % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF * HALVES + 4 + 1;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF * HALVES + 2 * SLOTS + 1;
   static constexpr int SMEM_BYTES = OFF_BAR + NUM_BARS * 8 + 16 + 1024;  // + alignment slack
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
@@ -578,9 +585,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* empty_bar = full_bar + STAGES;
   uint64_t* tfull_bar = empty_bar + STAGES;
   uint64_t* tempty_bar = tfull_bar + NBUF * HALVES;
-  uint64_t* sfull_bar = tempty_bar + NBUF * HALVES;  // [2] a group of scales is there
-  uint64_t* sempty_bar = sfull_bar + 2;     // [2]
-  uint64_t* drain_bar = sempty_bar + 2;
+  uint64_t* sfull_bar = tempty_bar + NBUF * HALVES;  // [SLOTS] a group of scales is there
+  uint64_t* sempty_bar = sfull_bar + C::SLOTS;       // [SLOTS]
+  uint64_t* drain_bar = sempty_bar + C::SLOTS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -606,8 +613,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&tfull_bar[b], 1);
       mbar_init(&tempty_bar[b], (C::PAIR ? 2 : 1) * C::WARPS_PER_BUF);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&sfull_bar[b], 2);
+    for (int b = 0; b < C::SLOTS; ++b) {
+      mbar_init(&sfull_bar[b], 64);  // the lanes of two warps
       mbar_init(&sempty_bar[b], kAccWarps);
     }
     mbar_init(drain_bar, 1);
@@ -754,54 +761,51 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp < kAccWarp0) {
     // ------------------------------------------------------ scales and bias
-    // The two warps take 64 token rows each; a lane reads one of eight
-    // neighbouring scales of every fourth row.  (Read by the accumulating
-    // warps themselves, one scale per lane and block from 32 rows, the loads
-    // took as much of the shared-memory bandwidth as the copies.)
+    // The two warps take 64 token rows each; neighbouring lanes copy the scales
+    // of a row's neighbouring blocks, four bytes at a time (all that is known of
+    // their alignment), asynchronously.  (Read by the accumulating warps
+    // themselves, one scale per lane and block from 32 rows, the loads took as
+    // much of the shared-memory bandwidth as the copies.)
     reg_give<kRegsFirst>();
-    const int j = lane & (kGroup - 1), half = warp - kAuxWarp0;
-    const int r0 = half * (BM / 2) + lane / kGroup;
-    int slot = 0, parity = 0;
+    const int j = lane & (C::GROUP - 1), half = warp - kAuxWarp0;
+    const int r0 = half * (BM / 2) + lane / C::GROUP;
+    int slot = 0, bias_slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = unit0; ok && u < p.units; u += ustep, parity ^= 1) {
+    for (int u = unit0; ok && u < p.units; u += ustep, bias_slot = (bias_slot + 1) % C::SLOTS) {
       int m, n;
       tile_of(u, p, m, n);
       const int t0 = m * C::TILE_M + (C::PAIR ? static_cast<int>(rank) * BM : 0);
-      for (int k0 = kb0; k0 < kb1; k0 += kGroup) {
+      const int nb = min(n * C::BN / kFp8Block + half, (p.N - 1) / kFp8Block);
+      for (int k0 = kb0; k0 < kb1; k0 += C::GROUP) {
         const int kb = min(k0 + j, kb1 - 1);  // past the end: any value, it is not used
-        const int nb = min(n * C::BN / kFp8Block + half, (p.N - 1) / kFp8Block);
-        const float w = __ldg(p.s_w + static_cast<size_t>(nb) * p.kblocks + kb);
-        float* g = reinterpret_cast<float*>(smem + C::OFF_AUX + slot * kGroupBytes);
-#pragma unroll 1
-        for (int i0 = 0; ok && i0 < BM / 8; i0 += 8) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int t = min(t0 + r0 + 4 * (i0 + i), p.T - 1);
-            v[i] = __ldg(p.s_x + static_cast<size_t>(t) * p.kblocks + kb);
-          }
-          if (i0 == 0) ok = wait_all(&sempty_bar[slot], phase ^ 1, abort_flag, p.status, 37);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (ok) g[j * kGroupRow + r0 + 4 * (i0 + i)] = v[i];
-        }
+        ok = wait_all(&sempty_bar[slot], phase ^ 1, abort_flag, p.status, 37);
         if (!ok) break;
-        if (lane < kGroup) g[kGroup * kGroupRow + half * kGroup + j] = w;
+        float* g = reinterpret_cast<float*>(smem + C::OFF_AUX + slot * C::GROUP_BYTES);
+#pragma unroll 4
+        for (int r = r0; r < (half + 1) * (BM / 2); r += 32 / C::GROUP) {
+          const int t = min(t0 + r, p.T - 1);
+          copy_async_4(g + j * C::GROUP_ROW + r, p.s_x + static_cast<size_t>(t) * p.kblocks + kb);
+        }
+        if (lane < C::GROUP)
+          copy_async_4(g + C::GROUP * C::GROUP_ROW + half * C::GROUP + j,
+                       p.s_w + static_cast<size_t>(nb) * p.kblocks + kb);
         if (k0 == kb0 && p.bias && !C::SPLIT) {
           // the unit's bias, BN / 2 values from each warp (N % 8 == 0: the
           // 16-byte words are all in or all out)
           const int c = half * (C::BN / 2) + 8 * lane;
           if (lane < C::BN / 16 && n * C::BN + c < p.N)
-            *reinterpret_cast<uint4*>(smem + C::OFF_BIAS + (parity * C::BN + c) * 2) =
-                __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(p.bias) + n * C::BN + c));
+            copy_async_16(smem + C::OFF_BIAS + (bias_slot * C::BN + c) * 2,
+                          static_cast<const E*>(p.bias) + n * C::BN + c);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull_bar[slot]);
-        slot ^= 1;
-        phase ^= slot == 0;
+        copy_async_arrive(&sfull_bar[slot]);
+        if (++slot == C::SLOTS) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
     }
+    copy_async_wait();  // none is on its way when the CTA ends
   } else {
     // ------------------------------------------------------ accumulation
     reg_take<kRegsAcc>();
@@ -815,10 +819,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // the (pair's leader's) barriers that hand a buffer back
     const uint32_t release0 = C::PAIR ? mapa_shared(smem_u32(&tempty_bar[half]), 0)
                                       : smem_u32(&tempty_bar[half]);
-    int buf = 0, slot = 0, parity = 0;
+    int buf = 0, slot = 0, bias_slot = 0;
     uint32_t tphase = 0, sphase = 0;
     bool ok = true;
-    for (int u = unit0; ok && u < p.units; u += ustep, parity ^= 1) {
+    auto next_slot = [&] {
+      if (++slot == C::SLOTS) {
+        slot = 0;
+        sphase ^= 1;
+      }
+    };
+    for (int u = unit0; ok && u < p.units; u += ustep, bias_slot = (bias_slot + 1) % C::SLOTS) {
       int m, n;
       tile_of(u, p, m, n);
       const int t = m * C::TILE_M + (C::PAIR ? static_cast<int>(rank) * BM : 0) + row;
@@ -831,11 +841,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // the state of its accumulator buffer are asked for ahead of their use.
       const float* scales;  // of the current group
       auto factor_at = [&](int j, float& x, float& w) {
-        x = scales[j * kGroupRow + row];
-        w = scales[kGroup * kGroupRow + part * COLS / kFp8Block * kGroup + j];
+        x = scales[j * C::GROUP_ROW + row];
+        w = scales[C::GROUP * C::GROUP_ROW + part * COLS / kFp8Block * C::GROUP + j];
       };
       auto next_group = [&] {
-        scales = reinterpret_cast<const float*>(smem + C::OFF_AUX + slot * kGroupBytes);
+        scales = reinterpret_cast<const float*>(smem + C::OFF_AUX + slot * C::GROUP_BYTES);
         return wait_all(&sfull_bar[slot], sphase, abort_flag, p.status, 38);
       };
       if (!next_group()) break;
@@ -886,12 +896,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           if (c == 0 && more) {
             probe = mbar_test_wait(&tfull_bar[next_buf * HALVES + half], next_phase);
-            const int j = (kb + 1 - kb0) & (kGroup - 1);
+            const int j = (kb + 1 - kb0) & (C::GROUP - 1);
             if (j == 0) {  // the last block of a group: hand it back, take the next
               __syncwarp();
               if (lane == 0) mbar_arrive(&sempty_bar[slot]);
-              slot ^= 1;
-              sphase ^= slot == 0;
+              next_slot();
               ok &= next_group();
             }
             factor_at(j, fx, fw);
@@ -906,7 +915,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if constexpr (!C::SPLIT) {
         // Bias, rounding, and 32 bytes of a row per store: whole sectors, and
         // half of the shared-memory traffic that staging for a copy would take.
-        const uint8_t* bias = smem + C::OFF_BIAS + (parity * C::BN + part * COLS) * 2;
+        const uint8_t* bias = smem + C::OFF_BIAS + (bias_slot * C::BN + part * COLS) * 2;
         E* y = static_cast<E*>(p.Y) + static_cast<size_t>(t) * p.N + o0;
 #pragma unroll
         for (int c0 = 0; c0 < COLS; c0 += 64) {
@@ -943,8 +952,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty_bar[slot]);
-        slot ^= 1;
-        sphase ^= slot == 0;
+        next_slot();
       } else {
         // Four columns at a time, in turn to the CTAs of the cluster, as float4
         // [source][turn][thread]: neighbouring lanes, neighbouring words.
