@@ -463,10 +463,10 @@ cudaError_t launch_rows_any(const Fp8Params& p, cudaStream_t st) {
 // block, so the factor is one number per lane and stage.
 //
 // 4096 x 6144 x 18432 takes 419 us alone (2.2 PFLOP/s) and 490 to 505 in a row,
-// where power lowers the clock: 636 thousand cycles, of which the MMAs alone
-// are 383.  With parts left out (and the results wrong): without the FMAs 543,
-// without the output's stores 617, without both 470, without the scales' copies
-// too 413.  A block's sums wait for their MMAs, are loaded, added, and handed
+// where power lowers the clock: 628 thousand cycles, of which the MMAs alone
+// are 383.  Copies of it with parts left out, when it took 652: without the FMAs
+// 543, without the output's stores 617, without both 470, without the scales'
+// copies too 413.  A block's sums wait for their MMAs, are loaded, added, and handed
 // back across the pair, with two buffers to cover that: the FMAs (256 cycles per
 // block and scheduler at best, 512 the MMAs) lengthen it, the loads from tensor
 // memory do not.  Three to six stages, 12 or 16 accumulating warps (192 columns
@@ -572,6 +572,25 @@ __device__ __forceinline__ void add_bias(float (&v)[8], const uint4& bias) {
   unpack8<E>(bias, b);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] += b[i];
+}
+
+// A step of the transposition of 4 x 4 pieces (two words of 16 bytes each)
+// among four lanes: pieces i and i ^ BIT change places with those of the lane
+// BIT off, so that after both steps piece r of lane q is piece q of lane q ^ r.
+template <int BIT>
+__device__ __forceinline__ void swap_pieces(uint4 (&w)[8], bool upper) {
+  uint32_t* v = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i & BIT) continue;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t &lo = v[8 * i + k], &hi = v[8 * (i + BIT) + k];
+      const uint32_t keep = upper ? hi : lo;
+      hi = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, BIT);
+      lo = keep;
+    }
+  }
 }
 
 template <typename E, class C>
@@ -913,39 +932,46 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tmem_ld_wait();
       if (!ok) break;
       if constexpr (!C::SPLIT) {
-        // Bias, rounding, and 32 bytes of a row per store: whole sectors, and
-        // half of the shared-memory traffic that staging for a copy would take.
+        // Bias and rounding; then groups of four lanes exchange their rows'
+        // pieces of 16 columns, so that each stores the same piece of four
+        // rows: a store of the warp is eight lines of 128 bytes, not 32 pieces
+        // of them, and needs no staging in shared memory.
         const uint8_t* bias = smem + C::OFF_BIAS + (bias_slot * C::BN + part * COLS) * 2;
-        E* y = static_cast<E*>(p.Y) + static_cast<size_t>(t) * p.N + o0;
+        const int piece = lane & 3, first_t = t - piece;
+        E* y = static_cast<E*>(p.Y) + o0 + 16 * piece;
 #pragma unroll
         for (int c0 = 0; c0 < COLS; c0 += 64) {
-          uint4 bv[8] = {};  // ahead of the stores, all in flight together
+          uint4 bv[8] = {};  // ahead of their use, all in flight together
           if (p.bias) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               bv[i] = *reinterpret_cast<const uint4*>(bias + (c0 + 8 * i) * 2);
           }
+          uint4 w[8];
 #pragma unroll
-          for (int c = c0; c < c0 + 64; c += 16) {
-            uint4 w[2];
+          for (int i = 0; i < 8; ++i) {
+            float v[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float v[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack_f32x2(acc[c / 2 + 4 * h + i]);
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-              }
-              if (p.bias) add_bias<E>(v, bv[(c - c0) / 8 + h]);
-              w[h] = pack8<E>(v);
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = unpack_f32x2(acc[c0 / 2 + 4 * i + k]);
+              v[2 * k] = f.x;
+              v[2 * k + 1] = f.y;
             }
-            if (t < p.T) {  // N % 8 == 0: eight columns are all in or all out
-              if (p.wide && o0 + c + 8 < p.N) {
-                st_global_32(y + c, w[0], w[1]);
+            if (p.bias) add_bias<E>(v, bv[i]);
+            w[i] = pack8<E>(v);
+          }
+          swap_pieces<1>(w, piece & 1);
+          swap_pieces<2>(w, piece & 2);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {  // the row r lanes off in the group
+            const int row_t = first_t + (piece ^ r), o = o0 + c0 + 16 * piece;
+            if (row_t < p.T) {  // N % 8 == 0: eight columns are all in or all out
+              E* to = y + static_cast<size_t>(row_t) * p.N + c0;
+              if (p.wide && o + 8 < p.N) {
+                st_global_32(to, w[2 * r], w[2 * r + 1]);
               } else {
-                if (o0 + c < p.N) *reinterpret_cast<uint4*>(y + c) = w[0];
-                if (o0 + c + 8 < p.N) *reinterpret_cast<uint4*>(y + c + 8) = w[1];
+                if (o < p.N) *reinterpret_cast<uint4*>(to) = w[2 * r];
+                if (o + 8 < p.N) *reinterpret_cast<uint4*>(to + 8) = w[2 * r + 1];
               }
             }
           }
