@@ -462,7 +462,7 @@ cudaError_t launch_rows_any(const Fp8Params& p, cudaStream_t st) {
 // the next one.  A lane has one token row and the columns of one weight
 // block, so the factor is one number per lane and stage.
 //
-// 4096 x 6144 x 18432 takes 419 us alone (2.2 PFLOP/s) and 490 to 505 in a row,
+// 4096 x 6144 x 18432 takes 412 us alone (2.25 PFLOP/s) and 490 to 505 in a row,
 // where power lowers the clock: 628 thousand cycles, of which the MMAs alone
 // are 383.  Copies of it with parts left out, when it took 652: without the FMAs
 // 543, without the output's stores 617, without both 470, without the scales'
