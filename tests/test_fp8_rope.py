@@ -23,6 +23,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 import unittest.mock as mock
 
 import numpy as np
@@ -658,6 +659,43 @@ def test_kernels_with_tensor_memory_side_by_side(zq):
     torch.cuda.synchronize()
     for w, out in zip(want, got):
         assert all(torch.equal(w, y) for y in out)
+
+
+@pytest.mark.gpu
+def test_calls_from_several_threads(zq):
+    """Host threads call at once, each on a stream of its own: each gets what a
+    single thread gets."""
+    g = gen(9)
+    w = quantized(zq, torch.randn(768, 1024, generator=g), 128, 0)
+    gamma = torch.ones(1024, dtype=torch.float16, device="cuda")
+    pos, f = torch.arange(700, dtype=torch.int32, device="cuda"), zq.rope_frequencies(32)[0].cuda()
+    xs = [torch.randn(T, 1024, generator=g).half().cuda() for T in (1, 30, 100, 700)]
+
+    def layer(x):
+        T = x.shape[0]
+        y = zq.gemm_fp8(*zq.ln_quant_fp8(x, gamma), *w).view(T, 12, 64)
+        q, k = zq.qk_norm_rope(y[:, :8], y[:, 8:], pos[:T], f, norm=zq.NORM_RMS)
+        return y, q, k, *zq.bias_act_quant_fp8(x, None, zq.ACT_GELU)
+
+    want = [layer(x) for x in xs]
+    torch.cuda.synchronize()
+    wrong, streams = [], [torch.cuda.Stream() for _ in xs]
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            got = [layer(xs[(i + n) % 4]) for n in range(24)]
+        streams[i].synchronize()
+        for n, out in enumerate(got):
+            if not all(torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+                       for a, b in zip(out, want[(i + n) % 4])):
+                wrong.append((i, n))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 _FIRST_CALLS_IN_A_CAPTURE = r"""
