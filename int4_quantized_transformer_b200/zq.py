@@ -312,6 +312,7 @@ FP8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # zq_dtype
 _F32, _I32 = torch.float32, torch.int32
+_MOST = 2**31 - 1  # the sizes are C ints
 # the plain getters behind torch.cuda.current_device() and current_stream()
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -344,6 +345,8 @@ def _matrix(t, name: str):
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must have two dimensions, got {tuple(shape)}")
+    if shape[0] > _MOST or shape[1] > _MOST:
+        raise ValueError(f"{name} is too large: {tuple(shape)}")
     dev = _current_device()
     if not t.is_contiguous() or t.get_device() != dev:
         _ptr(t, t.dtype, shape, name, dev)
@@ -427,6 +430,8 @@ def gemm_fp8(Xq, s_x, Wq, s_w, bias=None, Y=None, out_dtype=torch.float16, strea
         raise ValueError(f"Xq and Wq must have two dimensions, got {tuple(xs)} and {tuple(ws)}")
     T, K = xs
     N = ws[0]
+    if T > _MOST or K > _MOST or N > _MOST:
+        raise ValueError(f"Xq or Wq is too large: {tuple(xs)} and {tuple(ws)}")
     kb, dev = -(-K // FP8_BLOCK), _current_device()
     x, sx = _ptr(Xq, FP8, xs, "Xq", dev), _ptr(s_x, _F32, (T, kb), "s_x", dev)
     w, sw = _ptr(Wq, FP8, (N, K), "Wq", dev), _ptr(s_w, _F32, (-(-N // FP8_BLOCK), kb), "s_w", dev)
@@ -523,6 +528,8 @@ def qk_norm_rope(q, k, positions, inv_freq, layout: int = ROPE_HALF, scale: floa
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a tensor of one dimension")
     T, _, D = q.shape
+    if T > _MOST or D > _MOST:
+        raise ValueError(f"q is too large: {tuple(q.shape)}")
     half, dev = inv_freq.shape[0], _current_device()
     pos = _ptr(positions, _I32, (T,), "positions", dev)
     f = _ptr(inv_freq, _F32, (half,), "inv_freq", dev)

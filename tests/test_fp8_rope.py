@@ -932,6 +932,23 @@ def test_binding_refuses_another_device(zq):
         zq._ptr(t, torch.float16, (4, 64), "X", 0)
 
 
+def test_binding_refuses_sizes_past_an_int(zq):
+    def huge(dtype, *shape):
+        t = mock.MagicMock(spec=torch.Tensor)
+        t.dtype, t.shape, t.is_cuda = dtype, torch.Size(shape), True
+        t.dim.return_value = len(shape)
+        return t
+
+    n, f = 2**32 + 3, torch.zeros(4)
+    x, w = huge(torch.float16, n, 64), huge(F8, 128, 64)
+    for call in (lambda: zq.ln_quant_fp8(x), lambda: zq.bias_act_quant_fp8(x),
+                 lambda: zq.quantize_weights_fp8(x), lambda: zq.gemm_fp8(huge(F8, n, 64), f, w, f),
+                 lambda: zq.gemm_fp8(w, f, huge(F8, n, 64), f),
+                 lambda: zq.qk_norm_rope(huge(torch.float16, n, 1, 64), None, f, f)):
+        with pytest.raises(ValueError, match="too large"):
+            call()
+
+
 @pytest.mark.gpu
 def test_binding_refuses_shapes_and_dtypes(zq):
     c = lambda *s, d=torch.float16: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
