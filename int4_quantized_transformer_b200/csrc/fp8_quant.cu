@@ -4,8 +4,9 @@
 // one scale for each 128 x 128 block.
 //
 // All three read their fp16 or bf16 input once into registers, reduce the
-// block maxima there, and write one byte per value and four per block, so
-// HBM traffic (3 bytes per value) is what bounds them.
+// block maxima there, and write one byte per value and four per block: HBM
+// traffic (3 bytes per value) bounds the weights and the rows as they are,
+// instructions the LayerNorm and the GeLU.
 #include <algorithm>
 
 #include "zq_fp8.cuh"
