@@ -174,30 +174,31 @@ __device__ __forceinline__ void tile_angles(const RopeParams& p, const Tile& t, 
 }
 
 // Without a norm; bound by HBM: 4096 tokens of 2 x 64 heads of 96, 24 rotated,
-// to another output in 39.8 us (5.1 TB/s, 0.77 of a copy), in place 23.  (Loads
-// that bypass L1 47.5 us; two or eight tokens ahead instead of four 38.4 and
-// 39.9, but 19.7 and 19.9 for the 18.9 us of 8192 tokens of 2 x 16 heads of 80.)
-// Threads of rotated units come first, then (to another output) threads that
-// copy the rest; each has the loads of AHEAD tokens in flight.  A token whose position is negative is passed over.
+// to another output in 37.6 us (5.4 TB/s, 0.82 of a copy).  (Loads that bypass
+// L1 took 8 us longer.)  Threads of rotated units come first, then (to another
+// output) threads that copy the rest; each has the loads of AHEAD tokens in
+// flight, the first ones during the sines: without that 8192 tokens of 40 heads
+// of 128 took 32.6 us, not 27.3, 1000 of 72 heads 13.5, not 10.3.  Four tokens
+// pay only where a unit is two values wide: 8192 tokens of 2 x 16 heads of 80
+// in 17.9 us, with two 21.2; 1000 tokens of 72 heads of 128 in 12.3.  A token whose position is negative is passed over.
 template <typename E, int CUT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   using C = CutOf<CUT>;
-  constexpr int VEC = C::VEC, TAIL = C::TAIL, ANG = C::ANGLES, AHEAD = 4;
+  constexpr int VEC = C::VEC, TAIL = C::TAIL, ANG = C::ANGLES, AHEAD = CUT == kHalf2 ? 4 : 2;
   __shared__ __align__(16) float cs[kMaxAngles], sn[kMaxAngles];
   __shared__ int pos[kMaxTokens];
   grid_dependency_wait();
   grid_launch_dependents();
   const Tile tl = tile_of(p);
-  tile_angles(p, tl, cs, sn, pos);
   const int heads = p.set[0].n + p.set[1].n, half = p.R / 2;
   const int ru = C::rotated_units(p.R), tu = p.copy_rest ? C::tail_units(p.D, p.R) : 0;
-  int c = tl.column * kThreads + static_cast<int>(threadIdx.x);
+  int c = tl.column * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
   const bool rotates = c < heads * ru;
   if (!rotates) c -= heads * ru;
   const int per_head = rotates ? ru : tu;
-  if (per_head == 0 || c >= heads * per_head) return;
-  int head = c / per_head;
-  const int u = c - head * per_head;
+  const bool live = per_head > 0 && c < heads * per_head;
+  int head = live ? c / per_head : 0;
+  const int u = live ? c - head * per_head : 0;
   const int which = head >= p.set[0].n;
   if (which) head -= p.set[0].n;
   const Heads& hd = p.set[which];
@@ -205,16 +206,25 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   const E* in = static_cast<const E*>(hd.in) + tl.token0 * hd.in_token + head * hd.in_head + at;
   E* out = static_cast<E*>(hd.out) + tl.token0 * hd.out_token + head * hd.out_head + at;
   const long long di = hd.in_token, od = hd.out_token;
+  uint32_t a[AHEAD][4], b[AHEAD][4];
+  auto fetch = [&](int t0, auto rotated) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (t0 + k < tl.tokens) {
+        load_words<decltype(rotated)::value ? VEC : TAIL>(in + k * di, a[k]);
+        if constexpr (decltype(rotated)::value && C::HALF)
+          load_words<VEC>(in + k * di + half, b[k]);
+      }
+    in += AHEAD * di;
+  };
+  // the first loads are on their way during the sines
+  if (live && rotates) fetch(0, std::true_type{});
+  if (live && !rotates) fetch(0, std::false_type{});
+  tile_angles(p, tl, cs, sn, pos);
+  if (!live) return;
   if (rotates) {
     for (int t0 = 0; t0 < tl.tokens; t0 += AHEAD) {
-      uint32_t a[AHEAD][VEC / 2], b[AHEAD][VEC / 2];
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (t0 + k < tl.tokens) {
-          load_words<VEC>(in + k * di, a[k]);
-          if constexpr (C::HALF) load_words<VEC>(in + k * di + half, b[k]);
-        }
-      in += AHEAD * di;
+      if (t0) fetch(t0, std::true_type{});
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
         if (t0 + k < tl.tokens && pos[t0 + k] >= 0) {
@@ -239,11 +249,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     }
   } else {
     for (int t0 = 0; t0 < tl.tokens; t0 += AHEAD) {
-      uint32_t a[AHEAD][TAIL / 2];
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (t0 + k < tl.tokens) load_words<TAIL>(in + k * di, a[k]);
-      in += AHEAD * di;
+      if (t0) fetch(t0, std::false_type{});
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
         if (t0 + k < tl.tokens && pos[t0 + k] >= 0) store_words<TAIL>(out, a[k]);
@@ -456,7 +462,9 @@ cudaError_t launch_cut(const RopeParams& p0, cudaStream_t st) {
            : heads * (C::rotated_units(p.R) + (p.copy_rest ? C::tail_units(p.D, p.R) : 0));
   // tokens of a CTA at most: their sines have to fit
   const int row = std::max(4, (p.R / 2 + 3) & ~3), most = std::min(kMaxTokens, kMaxAngles / row);
-  const int cta = NORM ? static_cast<int>(32 * norm_warps(p.T, (threads + 31) / 32, row)) : kThreads;
+  const long long warps = (threads + 31) / 32, rest_columns = (warps * 32 + kThreads - 1) / kThreads;
+  const int cta = static_cast<int>(
+      32 * (NORM ? norm_warps(p.T, warps, row) : (warps + rest_columns - 1) / rest_columns));
   const long long columns = (threads + cta - 1) / cta;
   if (NORM) {
     // whole waves of CTAs, the tokens spread over them evenly
@@ -465,12 +473,14 @@ cudaError_t launch_cut(const RopeParams& p0, cudaStream_t st) {
     const long long waves = (p.T - 1) / (tiles * most) + 1;
     p.tokens = static_cast<int>((p.T - 1) / (waves * tiles) + 1);
   } else {
-    // As many tokens as leave 20 CTAs for each SM.  Measured: 4096 tokens of
-    // 2 x 64 heads of 96 values, 4, 16 and 24 per SM: 46.8, 40.9 and 37.2 us,
-    // but 8192 tokens of 2 x 16 heads of 80 best with 16 (19.5 us); whole
-    // waves as above 42.6 to 45.4 and 19.2 us.
-    const long long want = 20ll * num_sms();
-    p.tokens = static_cast<int>(std::max(1ll, std::min<long long>(p.T * columns / want, most)));
+    // As many tokens as leave 20 CTAs of 256 threads for each SM, and two (the
+    // loads in flight) from half of that; in CTAs that fit the heads (4096
+    // tokens of 24 heads of 64, 96 threads each: 7.5 us, in CTAs of 256 15.1).
+    // 10, 14 and 26 for the 20 made up to 10% of difference either way from 1000
+    // to 16384 tokens; whole waves as above took up to 13% longer; 512 tokens of
+    // 128 heads of 96 took 9.8 us one at a time and 7.3 by twos.
+    const long long work = p.T * columns * cta / (static_cast<long long>(kThreads) * num_sms());
+    p.tokens = static_cast<int>(std::min<long long>(std::max(work / 20, work < 20 ? 1ll : 2ll), most));
   }
   const long long ctas = (static_cast<long long>(p.T) + p.tokens - 1) / p.tokens * columns;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
