@@ -1,0 +1,99 @@
+"""Edges of the block-scaled FP8 linear layer and of the query/key norm with
+rotation: ties between codes, values that are not finite, plans of the GEMM
+that only some sizes or options take, outputs on another stream, and a layer
+of the operators together with each stage left out in turn."""
+import torch
+import pytest
+
+from test_fp8_rope import (DTYPES, F8, _device_status_clean, block_max, blocks, e4m3_grid, gen,  # noqa: F401
+                           spread, zq)
+
+
+# ------------------------------------------------------------ codes of 16-bit values, ties among them
+
+def exact_codes(y, rows):
+    """The e4m3 values nearest to y * 448 / a, halves to the even code, from
+    16-bit values: |y| * 448 has at most 14 significant bits and the product of
+    a 5-bit middle between two codes with a 16, so that both sides of every
+    comparison are exact in 64 bits and nothing is divided."""
+    y = y.double()
+    amax = block_max(y, rows)
+    a = spread(torch.where(amax > 0, amax.clamp_min(2.0 ** -110), amax), rows, *y.shape)
+    num, grid = y.abs() * 448, e4m3_grid()
+    hi = torch.searchsorted(grid, (num / torch.where(a > 0, a, torch.ones_like(a))).contiguous())
+    hi = hi.clamp(1, 126)
+    hi = torch.where((hi < 126) & (num > grid[hi] * a), hi + 1, hi)
+    hi = torch.where((hi > 1) & (num <= grid[hi - 1] * a), hi - 1, hi)
+    mid = (grid[hi - 1] + grid[hi]) / 2 * a
+    code = torch.where((num > mid) | ((num == mid) & (hi % 2 == 0)), hi, hi - 1)
+    return torch.where(a > 0, grid[code] * torch.sign(y), torch.zeros_like(y)), (num == mid) & (a > 0)
+
+
+def tied(n, k, rows, dtype, seed):
+    """A matrix whose every value is a tie (bar each block's largest): in a
+    block with a = 7 j 2^e the middle m between two codes is met by
+    y = m j 2^e / 64.  j odd, so that 448 / a = 64 / (j 2^e) has no short form."""
+    g = gen(seed)
+    js = torch.tensor([3, 5, 7] if dtype is torch.bfloat16 else [3, 5, 7, 9, 11, 13, 19, 21, 27, 45, 63])
+    shape = (blocks(n) if rows > 1 else n, blocks(k))
+    j = js[torch.randint(0, len(js), shape, generator=g)].double()
+    e = torch.randint(-3, 4, shape, generator=g).double()
+    unit = spread(j * 2.0 ** e, rows, n, k)
+    grid = e4m3_grid()
+    at = torch.randint(8, 126, (n, k), generator=g)  # codes of four significant bits: the middle has five
+    y = (grid[at] + grid[at + 1]) / 2 * unit / 64
+    y = torch.where(torch.rand(n, k, generator=g) < 0.5, y, -y)
+    for r in range(shape[0]):
+        for c in range(shape[1]):
+            y[r * rows, c * 128] = 7 * j[r, c] * 2.0 ** e[r, c]
+    return y
+
+
+def test_tied_inputs_are_ties():
+    for dtype in DTYPES:
+        y = tied(256, 512, 128, dtype, 1)
+        if dtype is torch.float16:  # small enough to be exact there too
+            assert torch.equal(y.half().double()[y.abs() >= 2.0 ** -14], y[y.abs() >= 2.0 ** -14])
+        t = y.to(dtype)
+        want, tie = exact_codes(t, 128)
+        assert tie.float().mean() > 0.9
+        # one rounded factor 448 / a sends some of them to the other neighbour
+        a = spread(block_max(t.double(), 128), 128, *t.shape).float()
+        one = (t.float() * (448 / a)).to(F8).double()
+        wrong = (one != want) & tie
+        assert wrong.float().mean() > 0.001
+        assert torch.all((one == want) | tie)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_ties_go_to_the_even_code(zq, dtype):
+    """Codes of weights and of rows as they are, bit for bit: blocks of ties,
+    normal values, and blocks at both ends of the type's range."""
+    y = torch.cat((tied(384, 1040, 128, dtype, 1), torch.randn(400, 1040, generator=gen(2)).double() * 0.02)).to(dtype)
+    for got, rows in ((zq.quantize_weights_fp8(y.cuda()), 128), (zq.bias_act_quant_fp8(y.cuda()), 1),
+                      (zq.ln_quant_fp8(y.cuda()), 1)):
+        want, _ = exact_codes(y, rows)
+        assert torch.equal(got[0].cpu().double(), want)
+    rows = tied(300, 1040, 1, dtype, 3).to(dtype)
+    far = torch.randn(64, 1040, generator=gen(4))
+    far = torch.cat((far * 2.0 ** 125, far * 2.0 ** -108, far * 2.0 ** -130) if dtype is torch.bfloat16
+                    else (far * 2.0 ** 13, far * 2.0 ** -16, far * 2.0 ** -22)).to(dtype)
+    for x in (rows, far):
+        q, s = zq.bias_act_quant_fp8(x.cuda())
+        want, _ = exact_codes(x, 1)
+        assert torch.equal(q.cpu().double(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_the_same_codes_each_time(zq, dtype):
+    x = torch.randn(600, 2064, generator=gen(5)).to(dtype).cuda()
+    gamma = (1 + 0.1 * torch.randn(2064, generator=gen(6))).to(dtype).cuda()
+    calls = (lambda: zq.quantize_weights_fp8(x), lambda: zq.bias_act_quant_fp8(x),
+             lambda: zq.bias_act_quant_fp8(x, gamma, zq.ACT_GELU), lambda: zq.ln_quant_fp8(x, gamma, gamma))
+    for call in calls:
+        q, s = call()
+        for _ in range(20):
+            q2, s2 = call()
+            assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
