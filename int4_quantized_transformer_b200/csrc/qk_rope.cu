@@ -113,7 +113,9 @@ __device__ __forceinline__ void load_floats(const float* p, float* f) {
     f[0] = v.x, f[1] = v.y;
   }
 }
-// Rotates the pairs (x[i], y[i]), or the neighbours in x.
+// Rotates the pairs (x[i], y[i]), or the first `pairs` of four neighbours in x
+// (the ones behind belong to values that do not rotate; a rotation by nothing
+// would not leave them alone: 0 times an infinity next door is NaN).
 template <int N>
 __device__ __forceinline__ void rotate_halves(float* x, float* y, const float* c, const float* s) {
 #pragma unroll
@@ -123,12 +125,13 @@ __device__ __forceinline__ void rotate_halves(float* x, float* y, const float* c
     y[i] = y[i] * c[i] + v * s[i];
   }
 }
-__device__ __forceinline__ void rotate_neighbours(float* x, const float* c, const float* s) {
+__device__ __forceinline__ void rotate_neighbours(float* x, const float* c, const float* s,
+                                                  int pairs) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float v = x[2 * i];
-    x[2 * i] = v * c[i] - x[2 * i + 1] * s[i];
-    x[2 * i + 1] = x[2 * i + 1] * c[i] + v * s[i];
+    const float a = x[2 * i], b = x[2 * i + 1];
+    x[2 * i] = i < pairs ? a * c[i] - b * s[i] : a;
+    x[2 * i + 1] = i < pairs ? b * c[i] + a * s[i] : b;
   }
 }
 
@@ -137,7 +140,7 @@ __device__ __forceinline__ void rotate_neighbours(float* x, const float* c, cons
 // that its addresses move by one addition.  The tile's sines and cosines are
 // computed first, with all threads.
 struct Tile {
-  int column, tokens, row;  // row: angles of a token, padded with (1, 0)
+  int column, tokens, row;  // row: angles of a token, padded to vectors of four
   long long token0;
 };
 __device__ __forceinline__ Tile tile_of(const RopeParams& p) {
@@ -238,10 +241,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
             rotate_halves<VEC>(x, y, co, si);
             narrow<E, VEC>(y, b[k]);
             store_words<VEC>(out + half, b[k]);
-          } else {
-            rotate_neighbours(x, co, si);
+            narrow<E, VEC>(x, a[k]);
+          } else {  // a pair is a word: the ones behind R stay as they came
+            const int pairs = half - ANG * u;
+            rotate_neighbours(x, co, si, pairs);
+            uint32_t turned[VEC / 2];
+            narrow<E, VEC>(x, turned);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i)
+              if (i < pairs) a[k][i] = turned[i];
           }
-          narrow<E, VEC>(x, a[k]);
           store_words<VEC>(out, a[k]);
         }
         out += od;
@@ -405,12 +414,12 @@ __global__ void __launch_bounds__(32 * kNormWarps, kSmNormWarps / kNormWarps)
           if (oa[n] >= 0 && oa[n] < p.R) {
             load_floats<4>(ct + oa[n] / 2, co);
             load_floats<4>(st + oa[n] / 2, si);
-            rotate_neighbours(a[n], co, si);
+            rotate_neighbours(a[n], co, si, (p.R - oa[n]) / 2);
           }
           if (ob[n] >= 0 && ob[n] < p.R) {
             load_floats<4>(ct + ob[n] / 2, co);
             load_floats<4>(st + ob[n] / 2, si);
-            rotate_neighbours(b[n], co, si);
+            rotate_neighbours(b[n], co, si, (p.R - ob[n]) / 2);
           }
         }
         uint32_t va[WIDE / 2], vb[WIDE / 2];

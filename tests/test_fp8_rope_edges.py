@@ -97,3 +97,76 @@ def test_the_same_codes_each_time(zq, dtype):
         for _ in range(20):
             q2, s2 = call()
             assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+
+
+# ------------------------------------------------------------ values behind the rotated ones
+
+def odd_rest(T, H, D, R, dtype, seed):
+    """Heads whose values behind R hold infinities, NaN and zeros of either
+    sign, next to finite ones, and the same heads with zeros there."""
+    x = torch.randn(T, H, D, generator=gen(seed)).to(dtype)
+    plain = x.clone()
+    plain[..., R:] = 0
+    odd = torch.tensor([float("inf"), float("-inf"), float("nan"), 0.0, -0.0, -1.0, 1.0])
+    at = torch.randint(0, len(odd), (T, H, D - R), generator=gen(seed + 1))
+    x[..., R:] = torch.where(torch.rand(T, H, D - R, generator=gen(seed + 2)) < 0.7, odd[at],
+                             x[..., R:].float()).to(dtype)
+    x[:, 0, R], x[:, 0, R + 1] = 3.0, float("inf")  # the pair right behind R
+    x[:, 1, R], x[:, 1, R + 1] = float("nan"), 2.0
+    x[:, 2, R], x[:, 2, R + 1] = -0.0, -1.0
+    return x.cuda(), plain.cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("D,R", [(64, 4), (64, 12), (80, 20), (64, 6), (64, 30), (64, 62), (128, 64), (96, 24)])
+def test_values_behind_the_rotation_are_copied(zq, dtype, layout, in_place, D, R):
+    if layout == 0 and R % 4:
+        pytest.skip("halves are rotated in multiples of four values")
+    T, H = 19, 5
+    x, plain = odd_rest(T, H, D, R, dtype, D + R)
+    pos = torch.arange(3, 3 + T, dtype=torch.int32, device="cuda")
+    f = zq.rope_frequencies(R)[0].cuda()
+    want = zq.qk_norm_rope(plain, None, pos, f, layout)[0]
+    before = x.clone()
+    got = zq.qk_norm_rope(x, None, pos, f, layout, q_out=x if in_place else None)[0]
+    bits = lambda t: t.contiguous().view(torch.int16)  # noqa: E731
+    assert torch.equal(bits(got[..., R:]), bits(before[..., R:]))
+    assert torch.equal(bits(got[..., :R]), bits(want[..., :R]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("norm", [1, 2])
+@pytest.mark.parametrize("D,R", [(64, 4), (64, 12), (80, 20), (64, 6), (64, 30), (64, 62), (128, 64)])
+def test_values_behind_the_rotation_get_the_norm_alone(zq, dtype, layout, norm, D, R):
+    """An infinite bias behind R (the head itself is finite) reaches its own
+    value and no other: what the norm gives without any rotation."""
+    if layout == 0 and R % 4:
+        pytest.skip("halves are rotated in multiples of four values")
+    T, H = 19, 5
+    x = torch.randn(T, H, D, generator=gen(D + R)).to(dtype).cuda()
+    w = (1 + 0.1 * torch.randn(D, generator=gen(1))).to(dtype).cuda()
+    b = torch.zeros(D, dtype=dtype, device="cuda")
+    b[R + 1::2] = float("inf")
+    w[R::4], b[R::4] = 0.0, -0.0
+    pos = torch.arange(3, 3 + T, dtype=torch.int32, device="cuda")
+    f = zq.rope_frequencies(R)[0].cuda()
+    got = zq.qk_norm_rope(x, None, pos, f, layout, norm=norm, q_weight=w, q_bias=b)[0]
+    v = x.double()
+    v = v - (v.mean(-1, keepdim=True) if norm == 2 else 0)
+    v = v / torch.sqrt(v.square().mean(-1, keepdim=True) + 1e-6) * w.double() + b.double()
+    rest, want = got[..., R:].double(), v[..., R:]
+    assert torch.equal(torch.isinf(rest), torch.isinf(want)) and not torch.isnan(got).any()
+    ok = torch.isfinite(want)
+    # (D + 8) units of 2^-24 for the sums and two roundings, half a step of the
+    # type; the mean is off by D units of the mean magnitude, which is at most
+    # one standard deviation (and a little), times a weight below 2
+    tol = ((D + 10) * 2.0 ** -24 + torch.finfo(dtype).eps / 2) * want[ok].abs() + 2 * (D + 10) * 2.0 ** -24
+    assert torch.all((rest[ok] - want[ok]).abs() <= tol)
+    zero = (w == 0)[R:].expand_as(rest)
+    assert torch.all(rest[zero] == 0)
+    assert torch.isfinite(got[..., :R]).all()
