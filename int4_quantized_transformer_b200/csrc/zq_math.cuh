@@ -77,8 +77,10 @@ __device__ __forceinline__ float2 gelu_pair(float vx, float vy) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(px), "=f"(py) : "l"(p));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(px));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(py));
-  return make_float2(fmaf(-fabsf(vx), tx * ex, fmaxf(vx, 0.0f)),
-                     fmaf(-fabsf(vy), ty * ey, fmaxf(vy, 0.0f)));
+  // (+Inf: |v| h is Inf * 0 but for the bound; -Inf and NaN give NaN)
+  constexpr float kLargest = 0x1.fffffep127f;
+  return make_float2(fmaf(-fabsf(fminf(vx, kLargest)), tx * ex, fmaxf(vx, 0.0f)),
+                     fmaf(-fabsf(fminf(vy, kLargest)), ty * ey, fmaxf(vy, 0.0f)));
 }
 
 }  // namespace zq

@@ -170,3 +170,30 @@ def test_values_behind_the_rotation_get_the_norm_alone(zq, dtype, layout, norm, 
     zero = (w == 0)[R:].expand_as(rest)
     assert torch.all(rest[zero] == 0)
     assert torch.isfinite(got[..., :R]).all()
+
+
+# ------------------------------------------------------------ GeLU at the ends of its range
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_gelu_of_values_that_are_not_finite(zq, dtype, with_bias):
+    """GeLU(+Inf) is +Inf, and NaN stays NaN; -Inf times a probability of 0 is
+    NaN, as in the definition taken literally.  The block that holds one of
+    them has NaN codes, no other block does."""
+    inf, big = float("inf"), torch.finfo(dtype).max
+    x = torch.randn(5, 512, generator=gen(1)).to(dtype)
+    x[0, 130], x[1, 131], x[2, 132], x[3, 133], x[3, 140] = inf, -inf, float("nan"), big, -big
+    b = torch.zeros(512, dtype=dtype).cuda() if with_bias else None
+    y = torch.empty_like(x.cuda())
+    q, s = zq.bias_act_quant_fp8(x.cuda(), b, zq.ACT_GELU, y=y)
+    y, q, s = y.cpu(), q.cpu().double(), s.cpu()
+    assert y[0, 130] == inf and torch.isnan(y[1, 131]) and torch.isnan(y[2, 132])
+    assert y[3, 133] == big and y[3, 140] == 0
+    assert (~torch.isfinite(y)).sum() == 3
+    for r in range(5):
+        bad = torch.zeros(512, dtype=torch.bool)
+        bad[128:256] = r < 3
+        assert torch.equal(torch.isnan(q[r]), bad)
+        assert torch.equal(torch.isfinite(s[r]), ~bad[::128])
+    assert q[3, 133] == 448 and q[3, 140] == 0
