@@ -356,7 +356,7 @@ zq_status zq_bias_act_quant_fp8(const void* X, int dtype, const void* bias, int 
  * ZQ_OPT_SPLIT_K 1 to 8, at most KB: that many CTAs of a cluster share a tile
  * (or rows) along K; ZQ_OPT_GEMM_BN 128 or 256 and ZQ_OPT_CTA_PAIR as for
  * zq_gemm_w8a8: the tiles' width and pairs; ZQ_OPT_MAX_CTAS: CTAs of the
- * weight-row kernel.
+ * weight-row kernel (more where 128 rows each, or a forced split, need them).
  */
 zq_status zq_gemm_fp8(const void* Xq, const float* s_x, const void* Wq, const float* s_w,
                       const void* bias, int T, int N, int K, int dtype, void* Y,

@@ -428,8 +428,9 @@ template <typename E>
 cudaError_t launch_rows_any(const Fp8Params& p, cudaStream_t st) {
   const long long sms = num_sms();
   const int forced = option(ZQ_OPT_SPLIT_K), cap = option(ZQ_OPT_MAX_CTAS);
-  auto rows_for = [&](long long ctas) {
-    return static_cast<int>(std::min<long long>(128, (p.N + ctas * 8 - 1) / (ctas * 8) * 8));
+  auto rows_for = [&](long long ctas) {  // rows of each, if there were so many (no fewer than 1)
+    const long long eights = 8 * std::max(1ll, ctas);
+    return static_cast<int>(std::min<long long>(128, (p.N + eights - 1) / eights * 8));
   };
   // Two CTAs per SM stream large matrices best, one CTA small ones; K is
   // split until a CTA has 64 rows (8 KB to copy per block) or little of K.
@@ -440,9 +441,11 @@ cudaError_t launch_rows_any(const Fp8Params& p, cudaStream_t st) {
   const bool large = static_cast<long long>(p.N) * p.K >= (24ll << 20) || p.N > 128 * sms;
   const long long target = cap ? cap : (large ? 2 * sms : sms);
   int split = 1;
-  while (split < 8 && rows_for(target / split) < 64 && p.kblocks >= 4 * split) split *= 2;
+  while (split < 8 && 2 * split <= target && rows_for(target / split) < 64 &&
+         p.kblocks >= 4 * split)
+    split *= 2;
   if (forced) split = forced;
-  const int rows = rows_for(std::max<long long>(1, target / split));
+  const int rows = rows_for(target / split);
   auto go = [&](auto tn) {
     return launch_rows_gemm<E, RowsCfg<decltype(tn)::value>>(p, rows, split, st);
   };

@@ -2,11 +2,15 @@
 rotation: ties between codes, values that are not finite, plans of the GEMM
 that only some sizes or options take, outputs on another stream, and a layer
 of the operators together with each stage left out in turn."""
-import torch
-import pytest
+import os
+import subprocess
+import sys
 
-from test_fp8_rope import (DTYPES, F8, _device_status_clean, block_max, blocks, e4m3_grid, gen,  # noqa: F401
-                           spread, zq)
+import pytest
+import torch
+
+from test_fp8_rope import (DTYPES, F8, _device_status_clean, block_max, blocks, check_gemm,  # noqa: F401
+                           e4m3_grid, gen, spread, zq)
 
 
 # ------------------------------------------------------------ codes of 16-bit values, ties among them
@@ -197,3 +201,37 @@ def test_gelu_of_values_that_are_not_finite(zq, dtype, with_bias):
         assert torch.equal(torch.isnan(q[r]), bad)
         assert torch.equal(torch.isfinite(s[r]), ~bad[::128])
     assert q[3, 133] == 448 and q[3, 140] == 0
+
+
+# ------------------------------------------------------------ plans of the GEMM
+
+_EVERY_PLAN = r"""
+import itertools, sys
+sys.path.insert(0, {root!r})
+from int4_quantized_transformer_b200 import zq
+L, A = zq.lib(), 1 << 40  # an aligned address that is never dereferenced: there is no device
+for cap, split, bn, path, pair in itertools.product((0, 1, 2, 3, 7), (0, 1, 2, 3, 8), (0, 128, 256), (0, 1, 2),
+                                                    (0, 1, 2)):
+    with zq.options(max_ctas=cap, split_k=split, bn=bn, path=path, pair=pair):
+        for T, N, K in ((1, 8, 16), (16, 48, 512), (64, 8, 4096), (16, 2**31 - 8, 1024), (65, 24576, 1024),
+                        (300, 128, 24576), (2**31 - 1, 8, 16)):
+            rc = L.zq_gemm_fp8(A, A, A, A, None, T, N, K, 0, A, None)
+            assert rc in (zq.ZQ_ERR_UNSUPPORTED, zq.ZQ_ERR_CUDA), rc
+print("ok")
+"""
+
+
+def test_gemm_plans_on_the_host():
+    """Every plan is made without a division by zero (which would end the
+    process, so a process of its own makes them, where no device is seen)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", _EVERY_PLAN.format(root=root)], capture_output=True, text=True,
+                         timeout=300, env=dict(os.environ, CUDA_VISIBLE_DEVICES=""))
+    assert out.returncode == 0 and out.stdout.split()[-1:] == ["ok"], (out.returncode, out.stderr[-2000:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("max_ctas", [1, 2, 3])
+@pytest.mark.parametrize("T,K,N", [(1, 1024, 8), (16, 2064, 48), (33, 1024, 48), (64, 4096, 136)])
+def test_gemm_on_very_few_ctas(zq, max_ctas, T, K, N):
+    check_gemm(zq, T, K, N, torch.float16, path=2, max_ctas=max_ctas)
