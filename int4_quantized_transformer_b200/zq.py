@@ -6,6 +6,12 @@ and the current CUDA stream to the C ABI, and raises ``ZQError`` on a
 non-zero status.  All arithmetic happens in the CUDA kernels; there is no
 CPU or PyTorch fallback, and importing this module without a built
 ``libzq.so`` raises immediately.
+
+``stream=`` runs a call on another stream than the current one.  Outputs that
+are made by the call are then that stream's memory, as if they were made under
+``torch.cuda.stream(stream)``.  What the caller passes in has to stay alive
+until the stream is done with it (``Tensor.record_stream``), as for torch's own
+calls.
 """
 from __future__ import annotations
 
@@ -102,6 +108,16 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A new tensor for the call's output, of the memory of the stream that
+    writes it: the current stream's may still be in use by earlier work there,
+    and would be given out again before `stream` has finished."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t: torch.Tensor | None, dtype, shape, name: str):
     if t is None:
         return None
@@ -166,10 +182,10 @@ def quantize_weights_groupwise(W: torch.Tensor, g: int, bits: int, Wq=None, s_gr
     Returns (Wq, s_grp): int8 [N,K] (bits 8) or uint8 [N,K/2] (bits 4), fp32 [g]."""
     N, K = W.shape
     if Wq is None:
-        Wq = torch.empty((N, K) if bits == 8 else (N, K // 2),
-                         dtype=torch.int8 if bits == 8 else torch.uint8, device=W.device)
+        Wq = _empty((N, K) if bits == 8 else (N, K // 2), torch.int8 if bits == 8 else torch.uint8,
+                    W.device, stream)
     if s_grp is None:
-        s_grp = torch.empty(g, dtype=torch.float32, device=W.device)
+        s_grp = _empty(g, torch.float32, W.device, stream)
     wq_dtype = torch.int8 if bits == 8 else torch.uint8
     _check(_lib.zq_quantize_weights_groupwise(
         _dev(W, torch.float16, (N, K), "W"), N, K, g, bits,
@@ -184,9 +200,9 @@ def ln_quant(X: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, Xq=None,
     is quant-only.  Returns (Xq int8 [T,K], s_tok fp32 [T])."""
     T, K = X.shape
     if Xq is None:
-        Xq = torch.empty((T, K), dtype=torch.int8, device=X.device)
+        Xq = _empty((T, K), torch.int8, X.device, stream)
     if s_tok is None:
-        s_tok = torch.empty(T, dtype=torch.float32, device=X.device)
+        s_tok = _empty(T, torch.float32, X.device, stream)
     _check(_lib.zq_ln_quant(
         _dev(X, torch.float16, (T, K), "X"), _dev(gamma, torch.float16, (K,), "gamma"),
         _dev(beta, torch.float16, (K,), "beta"), T, K, float(eps),
@@ -205,9 +221,9 @@ def bias_act_quant(X: torch.Tensor, bias=None, act: int = ACT_NONE, Xq=None, s_t
     s_tok fp32 [T]); y, if given, receives the fp16 activation."""
     T, K = X.shape
     if Xq is None:
-        Xq = torch.empty((T, K), dtype=torch.int8, device=X.device)
+        Xq = _empty((T, K), torch.int8, X.device, stream)
     if s_tok is None:
-        s_tok = torch.empty(T, dtype=torch.float32, device=X.device)
+        s_tok = _empty(T, torch.float32, X.device, stream)
     _check(_lib.zq_bias_act_quant(
         _dev(X, torch.float16, (T, K), "X"), _dev(bias, torch.float16, (K,), "bias"), T, K,
         int(act), _dev(Xq, torch.int8, (T, K), "Xq"), _dev(s_tok, torch.float32, (T,), "s_tok"),
@@ -220,9 +236,9 @@ def static_quant(X: torch.Tensor, amax: float, Xq=None, s_tok=None, stream=None)
     (zq_static_quant).  Returns (Xq int8 [T,K], s_tok fp32 [T] = amax/127)."""
     T, K = X.shape
     if Xq is None:
-        Xq = torch.empty((T, K), dtype=torch.int8, device=X.device)
+        Xq = _empty((T, K), torch.int8, X.device, stream)
     if s_tok is None:
-        s_tok = torch.empty(T, dtype=torch.float32, device=X.device)
+        s_tok = _empty(T, torch.float32, X.device, stream)
     _check(_lib.zq_static_quant(
         _dev(X, torch.float16, (T, K), "X"), T, K, float(amax), _dev(Xq, torch.int8, (T, K), "Xq"),
         _dev(s_tok, torch.float32, (T,), "s_tok"), _stream(stream)), "zq_static_quant")
@@ -233,7 +249,7 @@ def _gemm(fn, what, Xq, s_tok, Wq, s_grp, bias, N, Y, acc, stream, bits):
     T, K = Xq.shape
     g = s_grp.shape[0]
     if Y is None:
-        Y = torch.empty((T, N), dtype=torch.float16, device=Xq.device)
+        Y = _empty((T, N), torch.float16, Xq.device, stream)
     wshape = (N, K) if bits == 8 else (N, K // 2)
     _check(fn(
         _dev(Xq, torch.int8, (T, K), "Xq"), _dev(s_tok, torch.float32, (T,), "s_tok"),
@@ -260,7 +276,7 @@ def widen_int4_weights(Wq4, K: int, Wq8=None, stream=None):
     """Packed INT4 codes uint8 [N, K/2] -> int8 codes [N, K] (zq_widen_int4_weights)."""
     N = Wq4.shape[0]
     if Wq8 is None:
-        Wq8 = torch.empty((N, K), dtype=torch.int8, device=Wq4.device)
+        Wq8 = _empty((N, K), torch.int8, Wq4.device, stream)
     _check(_lib.zq_widen_int4_weights(
         _dev(Wq4, torch.uint8, (N, K // 2), "Wq4"), N, K, _dev(Wq8, torch.int8, (N, K), "Wq8"),
         _stream(stream)), "zq_widen_int4_weights")
@@ -278,7 +294,7 @@ def _gemm_a16(fn, what, X, Wq, s_grp, bias, N, Y, acc, stream, bits):
     T, K = X.shape
     g = s_grp.shape[0]
     if Y is None:
-        Y = torch.empty((T, N), dtype=torch.float16, device=X.device)
+        Y = _empty((T, N), torch.float16, X.device, stream)
     wshape = (N, K) if bits == 8 else (N, K // 2)
     _check(fn(
         _dev(X, torch.float16, (T, K), "X"),
@@ -323,6 +339,25 @@ _new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_em
     or (lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda"))
 
 
+def _raw(stream, dev: int) -> int:
+    """The handle of the stream to run on, which has to be one of the current
+    device `dev`; None is that device's current stream."""
+    if stream is None:
+        return _current_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream must be on the current device cuda:{dev}, got {stream.device}")
+    return stream.cuda_stream
+
+
+def _out(shape, strides, dtype, dev, stream):
+    """A new tensor on the current device `dev` for the call's output (_empty)."""
+    if stream is None:
+        return _new(shape, strides, dtype)
+    _raw(stream, dev)
+    with torch.cuda.stream(stream):
+        return _new(shape, strides, dtype)
+
+
 def _ptr(t, dtype, shape, name: str, dev: int):
     """The data pointer of a contiguous tensor of this dtype and shape on the
     current device `dev` (the kernels run there); None stays None."""
@@ -353,16 +388,16 @@ def _matrix(t, name: str):
     return t.data_ptr(), d, shape[0], shape[1], dev
 
 
-def _fp8_out(rows, cols, scale_rows, Xq, s_blk, dev):
+def _fp8_out(rows, cols, scale_rows, Xq, s_blk, dev, stream):
     """Codes and scales (made where not given) and their pointers."""
     kb = -(-cols // FP8_BLOCK)
     if Xq is None:
-        Xq = _new((rows, cols), (cols, 1), FP8)
+        Xq = _out((rows, cols), (cols, 1), FP8, dev, stream)
         q = Xq.data_ptr()
     else:
         q = _ptr(Xq, FP8, (rows, cols), "Xq" if rows == scale_rows else "Wq", dev)
     if s_blk is None:
-        s_blk = _new((scale_rows, kb), (kb, 1), _F32)
+        s_blk = _out((scale_rows, kb), (kb, 1), _F32, dev, stream)
         s = s_blk.data_ptr()
     else:
         s = _ptr(s_blk, _F32, (scale_rows, kb), "s_blk", dev)
@@ -374,9 +409,9 @@ def quantize_weights_fp8(W: torch.Tensor, Wq=None, s_blk=None, stream=None):
     block (zq_quantize_weights_fp8).  Returns (Wq float8_e4m3fn [N,K],
     s_blk fp32 [ceil(N/128), ceil(K/128)])."""
     w, dt, N, K, dev = _matrix(W, "W")
-    Wq, s_blk, q, s = _fp8_out(N, K, -(-N // FP8_BLOCK), Wq, s_blk, dev)
+    Wq, s_blk, q, s = _fp8_out(N, K, -(-N // FP8_BLOCK), Wq, s_blk, dev, stream)
     rc = _lib.zq_quantize_weights_fp8(
-        w, dt, N, K, q, s, _current_stream(dev) if stream is None else stream.cuda_stream)
+        w, dt, N, K, q, s, _raw(stream, dev))
     if rc:
         _check(rc, "zq_quantize_weights_fp8")
     return Wq, s_blk
@@ -393,9 +428,9 @@ def ln_quant_fp8(X: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, Xq=N
     g = None if gamma is None else _ptr(gamma, e, (K,), "gamma", dev)
     b = None if beta is None else _ptr(beta, e, (K,), "beta", dev)
     y = None if y_ln is None else _ptr(y_ln, e, (T, K), "Y_ln", dev)
-    Xq, s_blk, q, s = _fp8_out(T, K, T, Xq, s_blk, dev)
+    Xq, s_blk, q, s = _fp8_out(T, K, T, Xq, s_blk, dev, stream)
     rc = _lib.zq_ln_quant_fp8(x, dt, g, b, T, K, eps, q, s, y,
-                              _current_stream(dev) if stream is None else stream.cuda_stream)
+                              _raw(stream, dev))
     if rc:
         _check(rc, "zq_ln_quant_fp8")
     return Xq, s_blk
@@ -409,9 +444,9 @@ def bias_act_quant_fp8(X: torch.Tensor, bias=None, act: int = ACT_NONE, Xq=None,
     x, dt, T, K, dev = _matrix(X, "X")
     b = None if bias is None else _ptr(bias, X.dtype, (K,), "bias", dev)
     ya = None if y is None else _ptr(y, X.dtype, (T, K), "Y_act", dev)
-    Xq, s_blk, q, s = _fp8_out(T, K, T, Xq, s_blk, dev)
+    Xq, s_blk, q, s = _fp8_out(T, K, T, Xq, s_blk, dev, stream)
     rc = _lib.zq_bias_act_quant_fp8(x, dt, b, T, K, act, q, s, ya,
-                                    _current_stream(dev) if stream is None else stream.cuda_stream)
+                                    _raw(stream, dev))
     if rc:
         _check(rc, "zq_bias_act_quant_fp8")
     return Xq, s_blk
@@ -437,12 +472,12 @@ def gemm_fp8(Xq, s_x, Wq, s_w, bias=None, Y=None, out_dtype=torch.float16, strea
     w, sw = _ptr(Wq, FP8, (N, K), "Wq", dev), _ptr(s_w, _F32, (-(-N // FP8_BLOCK), kb), "s_w", dev)
     b = None if bias is None else _ptr(bias, out_dtype, (N,), "bias", dev)
     if Y is None:
-        Y = _new((T, N), (N, 1), out_dtype)
+        Y = _out((T, N), (N, 1), out_dtype, dev, stream)
         y = Y.data_ptr()
     else:
         y = _ptr(Y, out_dtype, (T, N), "Y", dev)
     rc = _lib.zq_gemm_fp8(x, sx, w, sw, b, T, N, K, dt, y,
-                          _current_stream(dev) if stream is None else stream.cuda_stream)
+                          _raw(stream, dev))
     if rc:
         _check(rc, "zq_gemm_fp8")
     return Y
@@ -487,7 +522,7 @@ def _strided(v, shape, dtype, what, dev):
     return token if shape[0] > 1 else 0, head if shape[1] > 1 else 0, v.data_ptr()
 
 
-def _heads(t, out, weight, bias, T, D, dtype, name, dev):
+def _heads(t, out, weight, bias, T, D, dtype, name, dev, stream):
     """(zq_heads as bytes, out) of a strided [T, heads, D] tensor."""
     heads = 0
     if isinstance(t, torch.Tensor):
@@ -498,7 +533,7 @@ def _heads(t, out, weight, bias, T, D, dtype, name, dev):
     it, ih, i = _strided(t, shape, dtype, name, dev)
     if out is None:
         ot, oh = heads * D, D
-        out = _new(shape, (ot, oh, 1), dtype)
+        out = _out(shape, (ot, oh, 1), dtype, dev, stream)
         o = out.data_ptr()
     else:
         ot, oh, o = _strided(out, shape, dtype, name + "_out", dev)
@@ -535,12 +570,12 @@ def qk_norm_rope(q, k, positions, inv_freq, layout: int = ROPE_HALF, scale: floa
     f = _ptr(inv_freq, _F32, (half,), "inv_freq", dev)
     if pos is None:
         raise TypeError("positions must be a CUDA tensor")
-    hq, q_out = _heads(q, q_out, q_weight, q_bias, T, D, e, "q", dev)
+    hq, q_out = _heads(q, q_out, q_weight, q_bias, T, D, e, "q", dev, stream)
     hk = None
     if k is not None:
-        hk, k_out = _heads(k, k_out, k_weight, k_bias, T, D, e, "k", dev)
+        hk, k_out = _heads(k, k_out, k_weight, k_bias, T, D, e, "k", dev, stream)
     rc = _lib.zq_qk_norm_rope(hq, hk, dt, T, D, norm, eps, pos, f, 2 * half, layout, scale,
-                              _current_stream(dev) if stream is None else stream.cuda_stream)
+                              _raw(stream, dev))
     if rc:
         _check(rc, "zq_qk_norm_rope")
     return q_out, k_out

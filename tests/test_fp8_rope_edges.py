@@ -5,6 +5,7 @@ of the operators together with each stage left out in turn."""
 import os
 import subprocess
 import sys
+import unittest.mock as mock
 
 import pytest
 import torch
@@ -235,3 +236,92 @@ def test_gemm_plans_on_the_host():
 @pytest.mark.parametrize("T,K,N", [(1, 1024, 8), (16, 2064, 48), (33, 1024, 48), (64, 4096, 136)])
 def test_gemm_on_very_few_ctas(zq, max_ctas, T, K, N):
     check_gemm(zq, T, K, N, torch.float16, path=2, max_ctas=max_ctas)
+
+
+# ------------------------------------------------------------ outputs on another stream
+
+def output_calls(zq, T=300, K=1024, N=768):
+    """Every call that makes its output: (bytes of an output, call with stream=)."""
+    g = gen(1)
+    x = torch.randn(T, K, generator=g).half().cuda()
+    w = torch.randn(N, K, generator=g).half().cuda()
+    b = torch.randn(K, generator=g).half().cuda()
+    q8, s8 = zq.bias_act_quant_fp8(x)
+    w8, sw = zq.quantize_weights_fp8(w)
+    qi, si = zq.ln_quant(x)
+    wi, sg = zq.quantize_weights_groupwise(w, 16, 8)
+    w4, sg4 = zq.quantize_weights_groupwise(w, 16, 4)
+    heads = torch.randn(T, 16, 64, generator=g).half().cuda()
+    pos, f = torch.arange(T, dtype=torch.int32, device="cuda"), zq.rope_frequencies(64)[0].cuda()
+    return {
+        "quantize_weights_fp8": lambda s: zq.quantize_weights_fp8(w, stream=s),
+        "ln_quant_fp8": lambda s: zq.ln_quant_fp8(x, b, b, stream=s),
+        "bias_act_quant_fp8": lambda s: zq.bias_act_quant_fp8(x, b, zq.ACT_GELU, stream=s),
+        "gemm_fp8": lambda s: zq.gemm_fp8(q8, s8, w8, sw, stream=s),
+        "qk_norm_rope": lambda s: zq.qk_norm_rope(heads[:, :8], heads[:, 8:], pos, f, stream=s),
+        "quantize_weights_groupwise": lambda s: zq.quantize_weights_groupwise(w, 16, 8, stream=s),
+        "ln_quant": lambda s: zq.ln_quant(x, b, b, stream=s),
+        "bias_act_quant": lambda s: zq.bias_act_quant(x, b, zq.ACT_GELU, stream=s),
+        "static_quant": lambda s: zq.static_quant(x, 4.0, stream=s),
+        "gemm_w8a8": lambda s: zq.gemm_w8a8(qi, si, wi, sg, stream=s),
+        "gemm_w4a8": lambda s: zq.gemm_w4a8(qi, si, w4, sg4, stream=s),
+        "gemm_w8a16": lambda s: zq.gemm_w8a16(x, wi, sg, stream=s),
+        "widen_int4_weights": lambda s: zq.widen_int4_weights(w4, K, stream=s),
+    }
+
+
+CALLS = ["quantize_weights_fp8", "ln_quant_fp8", "bias_act_quant_fp8", "gemm_fp8", "qk_norm_rope",
+         "quantize_weights_groupwise", "ln_quant", "bias_act_quant", "static_quant", "gemm_w8a8", "gemm_w4a8",
+         "gemm_w8a16", "widen_int4_weights"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_are_memory_of_the_stream_that_writes_them(zq, name):
+    """A block that the current stream has just let go of (and may still write)
+    is not given to a call on another stream."""
+    call = output_calls(zq)[name]
+    tensors = lambda out: [t for t in (out if isinstance(out, tuple) else (out,))]  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    want = tensors(call(None))
+    let_go = {t.data_ptr() for t in want}
+    want = [t.cpu() for t in want]  # the device tensors go back to the current stream's memory
+    again = tensors(call(None))
+    assert {t.data_ptr() for t in again} & let_go  # which hands them out first
+    again = None
+    torch.cuda.synchronize()
+    got = tensors(call(side))
+    assert not {t.data_ptr() for t in got} & let_go
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_a_side_stream_inside_a_capture(zq):
+    calls = output_calls(zq)
+    want = [calls[n](None) for n in CALLS[:5]]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = [calls[n](side) for n in CALLS[:5]]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    flat = lambda outs: [t for o in outs for t in (o if isinstance(o, tuple) else (o,))]  # noqa: E731
+    for a, b in zip(flat(got), flat(want)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_a_stream_of_another_device_is_refused(zq):
+    stream = mock.MagicMock()
+    stream.device_index, stream.device, stream.cuda_stream = 1, "cuda:1", 0
+    assert zq._raw(stream, 1) == 0
+    with pytest.raises(ValueError, match="current device cuda:0"):
+        zq._raw(stream, 0)
+    with pytest.raises(ValueError, match="current device cuda:0"):
+        zq._out((2, 2), (2, 1), torch.float16, 0, stream)
