@@ -325,3 +325,84 @@ def test_a_stream_of_another_device_is_refused(zq):
         zq._raw(stream, 0)
     with pytest.raises(ValueError, match="current device cuda:0"):
         zq._out((2, 2), (2, 1), torch.float16, 0, stream)
+
+
+# ------------------------------------------------------------ plans of the GEMM that some sizes alone take
+
+def check_gemm_on_device(zq, T, K, N, dtype, bias=True, seed=0, **opts):
+    """As check_gemm, with the 64-bit reference on the device, for sizes that
+    take long on the host.  The same tolerance."""
+    g = torch.Generator(device="cuda").manual_seed(seed + 7 * T + 3 * K + N)
+    x = torch.randn(T, K, generator=g, device="cuda") * torch.exp(torch.randn(T, 1, generator=g, device="cuda"))
+    w = torch.randn(N, K, generator=g, device="cuda") * 0.02
+    # scales that differ from block to block: a wrong block's scale shows
+    sx = torch.exp(torch.randn(T, blocks(K), generator=g, device="cuda"))
+    sw = torch.exp(torch.randn(blocks(N), blocks(K), generator=g, device="cuda"))
+    xq, wq = (x * 20).clamp(-448, 448).to(F8), (w * 1000).clamp(-448, 448).to(F8)
+    b = (torch.randn(N, generator=g, device="cuda") * 0.5).to(dtype) if bias else None
+    sx *= 2.0 ** -12
+    sw *= 2.0 ** -6
+    with zq.options(**opts):
+        y = zq.gemm_fp8(xq, sx, wq, sw, b, out_dtype=dtype)
+        again = zq.gemm_fp8(xq, sx, wq, sw, b, out_dtype=dtype)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    X, W = xq.double() * spread(sx.double(), 1, T, K), wq.double() * spread(sw.double(), 128, N, K)
+    ref, mag = X @ W.T, X.abs() @ W.abs().T
+    if bias:
+        ref, mag = ref + b.double(), mag + b.double().abs()
+    u = 2.0 ** -24
+    tol = (2 * 128 + 4 + blocks(K)) * u * mag
+    half, tiny = (2.0 ** -11, 2.0 ** -25) if dtype is torch.float16 else (2.0 ** -8, 2.0 ** -134)
+    tol = tol + half * (ref.abs() + tol) + tiny
+    err = (y.double() - ref).abs()
+    assert torch.all(err <= tol), f"worst {(err / tol).max().item():.2f} of the tolerance"
+    return y
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("split", [2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("T,K,N,dtype", [(65, 1024, 136, torch.float16), (300, 2064, 520, torch.bfloat16),
+                                         (129, 4096, 264, torch.float16), (257, 5008, 1032, torch.bfloat16)])
+def test_gemm_tiles_shared_along_k(zq, split, T, K, N, dtype):
+    """Every cluster size, also those that do not divide the 16 pieces of a
+    warp's columns nor the blocks of K, with several rows of token tiles, cut
+    off at the end of N and of T."""
+    check_gemm_on_device(zq, T, K, N, dtype, bias=split % 2 == 0, path=1, split_k=split)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("split", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("T,K,N", [(1, 1024, 136), (20, 4112, 520), (64, 2064, 24)])
+def test_gemm_weight_rows_shared_along_k(zq, split, T, K, N):
+    check_gemm_on_device(zq, T, K, N, torch.float16 if split % 2 else torch.bfloat16, path=2, split_k=split)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N", [(100, 2304, 768), (200, 4096, 2048), (200, 4096, 1536), (397, 5008, 2120),
+                                   (160, 3584, 1280), (65, 12288, 640), (500, 1280, 896), (128, 2816, 2560)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gemm_plans_of_some_tokens(zq, T, K, N, dtype):
+    check_gemm_on_device(zq, T, K, N, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("opts", [dict(bn=128, pair=1), dict(bn=256, pair=1), dict(bn=128, pair=2),
+                                  dict(bn=256, pair=2), {}])
+@pytest.mark.parametrize("T,K,N", [(1500, 4224, 6152), (3100, 8336, 2568)])
+def test_gemm_tiles_with_several_groups_of_scales(zq, opts, T, K, N):
+    """More than 32 blocks along K (two and three groups of scales per tile) and
+    more tiles than CTAs, so that groups, bias and accumulator buffers go on
+    from tile to tile."""
+    opts = dict(path=1, **opts) if opts else {}
+    for i, dtype in enumerate(DTYPES):
+        check_gemm_on_device(zq, T, K, N, dtype, bias=i == 0, **opts)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("opts", [dict(bn=128, pair=1), dict(bn=256, pair=1), dict(bn=128, pair=2),
+                                  dict(bn=256, pair=2)])
+@pytest.mark.parametrize("T,K,N", [(1700, 65536, 520), (900, 180224, 264)])
+def test_gemm_groups_of_token_tiles(zq, opts, T, K, N):
+    """K so long that the token tiles run in groups (40 MB of activations
+    each), the last of them shorter; and groups of a single tile."""
+    check_gemm_on_device(zq, T, K, N, torch.bfloat16, path=1, **opts)
