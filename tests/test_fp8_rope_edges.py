@@ -10,8 +10,8 @@ import unittest.mock as mock
 import pytest
 import torch
 
-from test_fp8_rope import (DTYPES, F8, _device_status_clean, block_max, blocks, check_gemm,  # noqa: F401
-                           e4m3_grid, gen, spread, zq)
+from test_fp8_rope import (DTYPES, F8, HALF_STEP, TINY, U, _device_status_clean, block_max, blocks,  # noqa: F401
+                           check_gemm, e4m3_grid, gen, rotate_ref, spread, zq)
 
 
 # ------------------------------------------------------------ codes of 16-bit values, ties among them
@@ -406,3 +406,165 @@ def test_gemm_groups_of_token_tiles(zq, opts, T, K, N):
     """K so long that the token tiles run in groups (40 MB of activations
     each), the last of them shorter; and groups of a single tile."""
     check_gemm_on_device(zq, T, K, N, torch.bfloat16, path=1, **opts)
+
+
+# ------------------------------------------------------------ a layer of the operators together
+
+LAYER = dict(h=512, H=8, D=64, R=32, ffn=2048)
+STAGES = ("qkv", "rotation", "out", "up", "down")
+
+
+def layer_inputs(T, dtype):
+    h, ffn, D = LAYER["h"], LAYER["ffn"], LAYER["D"]
+    g = gen(T)
+    r = lambda *s, by=1.0, add=0.0: (torch.randn(*s, generator=g) * by + add).to(dtype)  # noqa: E731
+    W = {n: r(*s, by=0.05) for n, s in (("qkv", (3 * h, h)), ("out", (h, h)), ("up", (ffn, h)), ("down", (h, ffn)))}
+    return dict(x=r(T, h), W=W, bias={n: r(w.shape[0], by=0.3) for n, w in W.items()},
+                gamma=r(h, by=0.3, add=1.0), beta=r(h, by=0.3), qw=r(D, by=0.3, add=1.0), kw=r(D, by=0.3, add=1.0),
+                pos=torch.arange(100, 100 + T).int())
+
+
+def frequencies(zq):
+    return zq.rope_frequencies(LAYER["R"], 10000.0, zq.ROPE_YARN, 8.0, 1.0, 32.0, 4096)
+
+
+def codes_and_doubt(y, err):
+    """Dequantized e4m3 values of rows whose values are known to within `err`,
+    and by how much each may be off: its scale, and where the value lies next
+    to the middle between two codes the step between them."""
+    a = spread(block_max(y, 1), 1, *y.shape)
+    ea = spread(block_max(err, 1), 1, *y.shape)  # of the block's largest value
+    grid, v = e4m3_grid(), y.abs() * 448 / a
+    hi = torch.searchsorted(grid, v.contiguous()).clamp(1, 126)
+    mid, step = (grid[hi - 1] + grid[hi]) / 2, grid[hi] - grid[hi - 1]
+    code = torch.where(v > mid, grid[hi], grid[hi - 1])  # (at a tie either: it is in doubt)
+    slack = (err + y.abs() * (ea / a + 4 * U)) * 448 / a
+    off = torch.where((v - mid).abs() <= slack, step, torch.zeros_like(step)) + code * (ea / a + 2 * U)
+    return torch.sign(y) * code * a / 448, off * a / 448
+
+
+def layer_stage(zq, p, stage, seen, without=""):
+    """(result, bound on its error) of one stage in 64 bits, from what the
+    stages before it gave (`seen`), so that a rounding that falls the other way
+    there is not counted here.  `without` leaves a part out or puts a wrong one
+    in its place.  Bounds: as in test_layernorm and test_bias_and_gelu for the
+    values that are quantized, check_gemm's for the products, half a step of the
+    16-bit type for each rounding to it."""
+    D, R, dtype = LAYER["D"], LAYER["R"], p["x"].dtype
+    half, tiny = HALF_STEP[dtype], TINY[dtype]
+
+    def round16(v, e):
+        return v, e + half * (v.abs() + e) + tiny
+
+    def linear(y, err, n):
+        X, dX = codes_and_doubt(y, err)
+        W = exact_codes(p["W"][n], 128)[0] * spread(block_max(p["W"][n].double(), 128) / 448, 128, *p["W"][n].shape)
+        b = torch.zeros(len(W), dtype=torch.float64) if without == "biases" else p["bias"][n].double()
+        e = (dX + (2 * 128 + 8 + blocks(W.shape[1])) * U * (X.abs() + dX)) @ W.abs().T + 8 * U * b.abs()
+        return round16(X @ W.T + b, e)
+
+    def ln(v):
+        gamma = 1.0 if without == "gamma" else p["gamma"].double()
+        beta = 0.0 if without == "beta" else p["beta"].double()
+        mean, rstd = v.mean(-1, keepdim=True), 1 / torch.sqrt(v.var(-1, correction=0, keepdim=True) + 1e-5)
+        if without == "LayerNorm":
+            mean, rstd = torch.zeros_like(mean), torch.ones_like(rstd)
+        mag = (v.abs() + v.abs().mean(-1, keepdim=True)) * rstd * p["gamma"].double().abs() + p["beta"].double().abs()
+        return (v - mean) * rstd * gamma + beta, 64 * U * mag
+
+    def plus(ve, other):  # the residual, added to what was rounded
+        return round16(ve[0] + other, ve[1])
+
+    if stage == "qkv":
+        return linear(*ln(p["x"].double()), "qkv")
+    if stage == "rotation":
+        f, scale = frequencies(zq)
+        x = seen["qkv"].view(-1, 3, LAYER["H"], D)
+        out, err = [], []
+        for i, w in ((0, "qw"), (1, "kw")):
+            pos = p["pos"] + (1 if without == "position" else 0)
+            v, e = rotate_ref(x[:, i], pos, f * (0 if without == "rotation" else 1), 0 if without == "layout" else 1,
+                              1.0 if without in ("scale", "rotation") else scale, 0 if without == "head norm" else 1,
+                              1e-6, None if without == "head weight" else p[w], None)
+            out.append(v), err.append(e)
+        return round16(torch.cat(out, 1).flatten(1), torch.cat(err, 1).flatten(1))
+    if stage == "out":
+        y = seen["mixed"].double()
+        return plus(linear(y, torch.zeros_like(y), "out"), p["x"].double())
+    if stage == "up":
+        return linear(*ln(seen["out"].double()), "up")
+    v = seen["up"].double()
+    y = 0.5 * v * torch.erfc(v * -(0.5 ** 0.5))
+    err = (1e-6 + 1.5 * U * v.square()) * y.abs()
+    if without in ("GeLU", "ReLU"):
+        y = v if without == "GeLU" else v.clamp_min(0)
+    res = plus(linear(y, err, "down"), seen["out"].double())
+    return (res[0] - seen["out"].double(), res[1]) if without == "residual" else res
+
+
+WITHOUT = {"biases": STAGES[:1] + STAGES[2:], "LayerNorm": ("qkv", "up"), "gamma": ("qkv", "up"), "beta": ("qkv", "up"),
+           "head norm": STAGES[1:2], "head weight": STAGES[1:2], "rotation": STAGES[1:2], "layout": STAGES[1:2],
+           "scale": STAGES[1:2], "position": STAGES[1:2], "GeLU": STAGES[4:], "ReLU": STAGES[4:],
+           "residual": STAGES[4:]}
+
+
+def layer_seen_by_definition(zq, p):
+    seen = {}
+    for stage in STAGES:
+        if stage == "out":
+            q, k = seen["rotation"].chunk(2, 1)
+            seen["mixed"] = q + k + seen["qkv"].chunk(3, 1)[2]
+        seen[stage] = layer_stage(zq, p, stage, seen)[0].to(p["x"].dtype)
+    return seen
+
+
+def outside(zq, p, stage, seen, without=""):
+    """The share of a stage's values that lie outside their bound."""
+    want, err = layer_stage(zq, p, stage, seen, without)
+    return float(((seen[stage].double() - want).abs() > err).float().mean())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [1, 7, 150])
+def test_layer_bounds_tell_a_missing_part(zq, T, dtype):
+    p = layer_inputs(T, dtype)
+    seen = layer_seen_by_definition(zq, p)
+    for stage in STAGES:
+        assert outside(zq, p, stage, seen) == 0
+    for part, stages in WITHOUT.items():
+        for stage in stages:
+            assert outside(zq, p, stage, seen, part) > 0.1, (part, stage)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [1, 7, 150])
+def test_layer_stage_by_stage(zq, T, dtype):
+    """LayerNorm, QKV projection, norm and rotation of the heads (in place),
+    output projection, LayerNorm, FFN with GeLU, run as a layer runs them:
+    every value of every stage within its bound, and outside it for the stage
+    with a part missing."""
+    H, D = LAYER["H"], LAYER["D"]
+    p = layer_inputs(T, dtype)
+    Q = {n: zq.quantize_weights_fp8(w.cuda()) for n, w in p["W"].items()}
+    linear = lambda q, s, n: zq.gemm_fp8(q, s, *Q[n], p["bias"][n].cuda(), out_dtype=dtype)  # noqa: E731
+    f, scale = frequencies(zq)
+    x, gamma, beta = p["x"].cuda(), p["gamma"].cuda(), p["beta"].cuda()
+    qkv = linear(*zq.ln_quant_fp8(x, gamma, beta), "qkv")
+    seen = {"qkv": qkv.clone()}
+    heads = qkv.view(T, 3, H, D)
+    q, k = zq.qk_norm_rope(heads[:, 0], heads[:, 1], p["pos"].cuda(), f.cuda(), zq.ROPE_INTERLEAVED, scale,
+                           zq.NORM_RMS, q_weight=p["qw"].cuda(), k_weight=p["kw"].cuda(),
+                           q_out=heads[:, 0], k_out=heads[:, 1])
+    assert torch.equal(heads[:, 2], seen["qkv"].view(T, 3, H, D)[:, 2])
+    seen["rotation"] = torch.cat((q, k), 1).flatten(1)
+    seen["mixed"] = (q + k + heads[:, 2]).reshape(T, -1).contiguous()  # in attention's place
+    seen["out"] = linear(*zq.bias_act_quant_fp8(seen["mixed"]), "out") + x
+    seen["up"] = linear(*zq.ln_quant_fp8(seen["out"], gamma, beta), "up")
+    seen["down"] = linear(*zq.bias_act_quant_fp8(seen["up"], None, zq.ACT_GELU), "down") + seen["out"]
+    seen = {n: t.cpu() for n, t in seen.items()}
+    for stage in STAGES:
+        assert outside(zq, p, stage, seen) == 0, stage
+    for part, stages in WITHOUT.items():
+        for stage in stages:
+            assert outside(zq, p, stage, seen, part) > 0.1, (part, stage)
