@@ -160,10 +160,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 }
 // As mbar_arrive_cluster for a thread that hands on tensor memory it has read,
 // and no data in other memory: tcgen05.wait::ld and the tcgen05 fence order
-// that, and the cluster-wide release of all its memory accesses (which waits
-// for them, about a microsecond on a busy SM) is left out.
+// that, so the arrival is relaxed, at cluster scope (a cluster-wide release of
+// all its memory accesses waits for them, about a microsecond on a busy SM).
 __device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
