@@ -204,6 +204,26 @@ def test_gelu_of_values_that_are_not_finite(zq, dtype, with_bias):
     assert q[3, 133] == 448 and q[3, 140] == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gelu_of_every_value(zq, dtype):
+    """Every finite value of the type, the far tail among them: 1e-6 for the
+    approximation, 1.5 units of 2^-24 of v^2 for the exponent's roundings, a
+    rounding of fp32 and half a step of the type.  A result below 7e-39 may be
+    flushed to 0."""
+    x = torch.arange(-2 ** 15, 2 ** 15).short().view(dtype)
+    x = x[torch.isfinite(x)]
+    x = torch.nn.functional.pad(x, (0, -len(x) % 128)).view(-1, 128)
+    y = torch.empty_like(x.cuda())
+    zq.bias_act_quant_fp8(x.cuda(), None, zq.ACT_GELU, y=y)
+    v = x.double()
+    want = 0.5 * v * torch.erfc(v * -(0.5 ** 0.5))
+    tol = (1e-6 + U * (1 + 1.5 * v.square().clamp_max(400)) + HALF_STEP[dtype]) * want.abs() + TINY[dtype]
+    tol += torch.where(want.abs() < 7e-39, want.abs(), torch.zeros_like(want))
+    bad = (y.cpu().double() - want).abs() > tol
+    assert not bad.any(), (x[bad][:5], y.cpu()[bad][:5])
+
+
 # ------------------------------------------------------------ plans of the GEMM
 
 _EVERY_PLAN = r"""
