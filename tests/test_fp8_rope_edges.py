@@ -588,3 +588,84 @@ def test_layer_stage_by_stage(zq, T, dtype):
     for part, stages in WITHOUT.items():
         for stage in stages:
             assert outside(zq, p, stage, seen, part) > 0.1, (part, stage)
+
+
+# ------------------------------------------------------------ offsets past 32 bits, and heads that are not there
+
+@pytest.mark.gpu
+def test_quantizers_past_32_bits(zq):
+    """More than 2^31 values: the last rows as in a call of their own."""
+    T, K = 70016, 32768
+    x = torch.randn(4096, K, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").half()
+    big = x.repeat(18, 1)[:T].contiguous()
+    gamma = (1 + 0.1 * torch.randn(K, generator=gen(2))).half().cuda()
+    assert T * K > 2 ** 31
+    for call in (lambda v: zq.ln_quant_fp8(v, gamma, gamma), lambda v: zq.bias_act_quant_fp8(v, gamma, zq.ACT_GELU),
+                 lambda v: zq.bias_act_quant_fp8(v)):
+        q, s = call(big)
+        for a, b in ((0, 3), (T // 2, T // 2 + 3), (T - 5, T)):
+            qc, sc = call(big[a:b])
+            assert torch.equal(q[a:b].view(torch.uint8), qc.view(torch.uint8)) and torch.equal(s[a:b], sc)
+        del q, s
+    q, s = zq.quantize_weights_fp8(big)
+    for a in (0, 65536 - 128, T - 128):  # whole blocks of rows
+        qc, sc = zq.quantize_weights_fp8(big[a:a + 128])
+        assert torch.equal(q[a:a + 128].view(torch.uint8), qc.view(torch.uint8))
+        assert torch.equal(s[a // 128:a // 128 + 1], sc)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N", [(140000, 16, 16384), (70016, 32768, 16), (33, 32768, 70016), (3, 32768, 70016)])
+def test_gemm_past_32_bits(zq, T, K, N):
+    """More than 2^31 outputs, activations or weights: the last rows and columns
+    against 64 bits (inputs of few values, so that every sum is exact)."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    mk = lambda r: torch.randint(-1, 2, (r, K), generator=g, device="cuda", dtype=torch.int8).to(F8)  # noqa: E731
+    x, w = mk(T), mk(N)
+    sx, sw = torch.ones(T, blocks(K), device="cuda"), torch.ones(blocks(N), blocks(K), device="cuda")
+    assert max(T * K, N * K, T * N) > 2 ** 31
+    y = zq.gemm_fp8(x, sx, w, sw)
+    rows = torch.tensor(sorted({0, T // 2, T - 1} | {r for r in (T - 130, T - 129) if r >= 0}), device="cuda")
+    cols = torch.tensor(sorted({0, N // 2, N - 1} | {c for c in (N - 130, N - 9) if c >= 0}), device="cuda")
+    want = (x[rows].double() @ w.double().T if N * K < 2 ** 30 else None)
+    if want is not None:
+        assert torch.equal(y[rows].double(), want)
+    want = x.double() @ w[cols].double().T if T * K < 2 ** 30 else x[rows].double() @ w[cols].double().T
+    got = y[:, cols] if T * K < 2 ** 30 else y[rows][:, cols]
+    assert want.abs().max() <= 2048  # exact in fp16
+    assert torch.equal(got.double(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", [0, 1])
+def test_rope_past_32_bits(zq, norm):
+    T, H, D = 270000, 64, 128
+    x = torch.randn(2000, H, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").half()
+    x = x.repeat(135, 1, 1)
+    assert T * H * D > 2 ** 31 and len(x) == T
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    f = zq.rope_frequencies(D)[0].cuda()
+    out = zq.qk_norm_rope(x[:, :40], x[:, 40:], pos, f, norm=norm)
+    for a, b in ((0, 3), (T // 2, T // 2 + 3), (T - 5, T)):
+        part = zq.qk_norm_rope(x[a:b, :40], x[a:b, 40:], pos[a:b], f, norm=norm)
+        assert torch.equal(out[0][a:b], part[0]) and torch.equal(out[1][a:b], part[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("norm", [0, 1, 2])
+def test_rope_without_queries_or_without_rotation(zq, layout, norm):
+    x = torch.randn(21, 6, 72, generator=gen(1)).half().cuda()
+    pos = torch.arange(21, dtype=torch.int32, device="cuda")
+    f = zq.rope_frequencies(24)[0].cuda()
+    want = zq.qk_norm_rope(x, None, pos, f, layout, norm=norm)[0]
+    q, k = zq.qk_norm_rope(x[:, :0], x, pos, f, layout, norm=norm)
+    assert q.shape == (21, 0, 72) and torch.equal(k, want)
+    q, k = zq.qk_norm_rope(x, x[:, :0], pos, f, layout, norm=norm)
+    assert k.shape == (21, 0, 72) and torch.equal(q, want)
+    none = torch.empty(0, device="cuda")
+    q, _ = zq.qk_norm_rope(x, None, pos, none, layout, norm=norm)
+    if norm == 0:
+        assert torch.equal(q, x)
+    assert torch.equal(q[..., 24:], want[..., 24:])
+    assert torch.equal(q[0], want[0])  # position 0
