@@ -371,7 +371,8 @@ zq_status zq_gemm_fp8(const void* Xq, const float* s_x, const void* Wq, const fl
  *              `dtype`; value d of head h of token t is at
  *              t * token_stride + h * head_stride + d (strides in elements).
  *              out == in (with equal strides) works in place; other overlaps
- *              of in and out are not allowed.
+ *              of in and out, and of the queries' with the keys', are not
+ *              allowed (the same address is refused: ZQ_ERR_SHAPE).
  *   norm       ZQ_NORM_NONE, ZQ_NORM_RMS (x / sqrt(mean(x^2) + eps)) or
  *              ZQ_NORM_LAYER ((x - mean) / sqrt(var + eps)) over the D values
  *              of a head, then weight[d] (NULL = 1) and bias[d] (NULL = 0);

@@ -559,6 +559,11 @@ extern "C" zq_status zq_qk_norm_rope(const zq_heads* q, const zq_heads* k, int d
   zq_status rc = check_heads(q, T, D, &p.set[0]);
   if (rc == ZQ_OK && k) rc = check_heads(k, T, D, &p.set[1]);
   if (rc != ZQ_OK || T == 0 || p.set[0].n + p.set[1].n == 0) return rc;
+  // what one set writes is not the other's to read or write
+  if (p.set[0].n && p.set[1].n &&
+      (p.set[0].out == p.set[1].out || p.set[0].out == p.set[1].in ||
+       p.set[1].out == p.set[0].in))
+    return ZQ_ERR_SHAPE;
   if (!positions || (R > 0 && !inv_freq)) return ZQ_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(positions) % 4 || reinterpret_cast<uintptr_t>(inv_freq) % 4)
     return ZQ_ERR_ALIGN;

@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from test_fp8_rope import (DTYPES, F8, HALF_STEP, TINY, U, _device_status_clean, block_max, blocks,  # noqa: F401
-                           check_gemm, e4m3_grid, gen, rotate_ref, spread, zq)
+                           check_gemm, e4m3_grid, gen, rope_call, rotate_ref, spread, zq)
 
 
 # ------------------------------------------------------------ codes of 16-bit values, ties among them
@@ -669,3 +669,16 @@ def test_rope_without_queries_or_without_rotation(zq, layout, norm):
         assert torch.equal(q, x)
     assert torch.equal(q[..., 24:], want[..., 24:])
     assert torch.equal(q[0], want[0])  # position 0
+
+
+def test_rope_refuses_one_memory_for_queries_and_keys(zq):
+    """Queries and keys written to the same place, or one of them over the
+    other's input, while both are at work."""
+    A, B, C = 1 << 40, 1 << 41, 1 << 42  # aligned addresses that are never dereferenced
+    for q, k in ((dict(i=A, o=B), dict(i=C, o=B)), (dict(i=A, o=A), dict(i=C, o=A)),
+                 (dict(i=A, o=C), dict(i=C, o=C)), (dict(i=A, o=B), dict(i=C, o=A)),
+                 (dict(i=A, o=B), dict(i=A, o=A))):
+        assert rope_call(zq, q=q, k=k) == zq.ZQ_ERR_SHAPE
+    # no keys, no tokens: nothing to refuse
+    assert rope_call(zq, q=dict(i=A, o=A), k=dict(i=A, o=A), T=0) == zq.ZQ_OK
+    assert rope_call(zq, q=dict(n=0), k=dict(n=0)) == zq.ZQ_OK
