@@ -61,6 +61,36 @@ cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& ready) {
   return e;
 }
 
+// Clusters of S CTAs of a kernel that the current device runs at once, as far
+// as the occupancy query knows: it counts one CTA of a kernel that allocates
+// tensor memory per SM.  Asked once per kernel, size and device (`known`).
+template <typename K>
+cudaError_t clusters_at_once(K* kernel, int threads, int smem, int S,
+                             std::atomic<int> (&known)[64][9], int* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev < 64 ? known[dev][S].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S * 64);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    n = std::max(n, 1);
+    if (dev < 64) known[dev][S].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
 // ------------------------------------------------------------ weight rows
 //
 // Up to 64 tokens: the weights' bytes bound the call, so they have to flow
@@ -424,27 +454,56 @@ cudaError_t launch_rows_gemm(const Fp8Params& p, int rows, int split, cudaStream
   return launch_pdl_cluster(kernel, dim3(grid), dim3(kRowsThreads), smem, st, split, mx, mw, rp);
 }
 
+// CTAs of the weight-row kernel in clusters of S that run at once, two to an
+// SM.  Clusters of four and eight leave SMs over: 72 of four (288 CTAs) took a
+// second wave, 70 did not, and the query says 66.
+template <typename E>
+cudaError_t rows_ctas_at_once(int S, long long* out) {
+  auto* kernel = fp8_rows_gemm_kernel<E, RowsCfg<16>>;
+  static std::atomic<int> known[64][9];
+  static std::atomic<uint64_t> ready{0};
+  int n = 0;
+  cudaError_t e = allow_smem(kernel, kRowsSmem, ready);
+  if (e == cudaSuccess) e = clusters_at_once(kernel, kRowsThreads, kRowsSmem, S, known, &n);
+  *out = std::min(2ll * n * S, 2ll * num_sms());
+  return e;
+}
+
 template <typename E>
 cudaError_t launch_rows_any(const Fp8Params& p, cudaStream_t st) {
-  const long long sms = num_sms();
   const int forced = option(ZQ_OPT_SPLIT_K), cap = option(ZQ_OPT_MAX_CTAS);
   auto rows_for = [&](long long ctas) {  // rows of each, if there were so many (no fewer than 1)
     const long long eights = 8 * std::max(1ll, ctas);
     return static_cast<int>(std::min<long long>(128, (p.N + eights - 1) / eights * 8));
   };
-  // Two CTAs per SM stream large matrices best, one CTA small ones; K is
-  // split until a CTA has 64 rows (8 KB to copy per block) or little of K.
-  // Measured at T = 16 (us): 24576 x 6144 with 280 CTAs of 88 rows 24.7, 147
-  // of 168 rows 26.9; 6144 x 24576 split in four, 280 CTAs, 26.2, in two, 140
-  // CTAs, 32.5, unsplit 55; 2120 x 5008 at T = 32 split in eight, 144 CTAs,
-  // 8.1, 272 CTAs 14.4, unsplit 16.2.
-  const bool large = static_cast<long long>(p.N) * p.K >= (24ll << 20) || p.N > 128 * sms;
-  const long long target = cap ? cap : (large ? 2 * sms : sms);
+  // One CTA per SM, or two where the weights are large; K is split until a CTA
+  // has 64 rows (8 KB to copy per block) or little of K.  Measured, one against
+  // two (us, N x K at T = 1, 16 and 40):
+  //   4096 x 4096 (16 M weights)   8.0 / 10.1    8.3 / 11.5   11.4 / 16.5
+  //   5120 x 5120, split           9.7 /  9.1   10.5 /  9.6   15.6 / 13.8
+  //   6144 x 24576, split         32.4 / 26.2   33.3 / 26.9   49.2 / 37.4
+  //   4096 x 8192, split further  10.7 / 11.3   11.4 / 11.7   16.6 / 17.4
+  //   12288 x 4096, unsplit       13.2 / 11.9   13.2 / 12.6   17.9 / 19.0
+  //   18432 x 6144, unsplit       21.4 / 20.3   21.6 / 20.4   26.0 / 33.7
+  //   16384 x 2048, short K        9.2 /  9.4    9.3 / 10.6   11.0 / 14.8
+  //   24576 x 6144, over 148 CTAs 25.6 / 24.8   25.7 / 24.7   34.0 / 33.5
+  const int alone = rows_for(num_sms());  // rows of a CTA with one per SM and all of K
+  const bool large =
+      static_cast<long long>(p.N) * p.K >= (24ll << 20) &&
+      (alone < 64 ? alone > 32
+                  : p.K >= 4096 && (p.T <= 32 || p.N > 128ll * num_sms()));
   int split = 1;
-  while (split < 8 && 2 * split <= target && rows_for(target / split) < 64 &&
-         p.kblocks >= 4 * split)
-    split *= 2;
-  if (forced) split = forced;
+  long long target = 0;  // CTAs of the launch
+  auto plan = [&](int S) {
+    split = S;
+    target = cap ? cap : num_sms();
+    return large && !cap ? rows_ctas_at_once<E>(S, &target) : cudaSuccess;
+  };
+  cudaError_t e = plan(forced ? forced : 1);
+  while (e == cudaSuccess && !forced && split < 8 && 2 * split <= target &&
+         rows_for(target / split) < 64 && p.kblocks >= 4 * split)
+    e = plan(2 * split);
+  if (e != cudaSuccess) return e;
   const int rows = rows_for(target / split);
   auto go = [&](auto tn) {
     return launch_rows_gemm<E, RowsCfg<decltype(tn)::value>>(p, rows, split, st);
@@ -1096,38 +1155,15 @@ cudaError_t launch_tile(const Fp8Params& p, int split, int* status, cudaStream_t
   return launch_pdl(kernel, dim3(grid), dim3(kTileThreads), C::SMEM_BYTES, st, mx, mw, tp);
 }
 
-// Clusters of S CTAs of the split tile that fit the current device at once
-// (asked once per size and device).
+// Clusters of S CTAs of the split tile that fit the current device at once.
 template <typename E>
 cudaError_t split_clusters(int S, int* out) {
   using C = TileCfg<128, false, true>;
   auto* kernel = fp8_tile_kernel<E, C>;
   static std::atomic<int> known[64][9];
   static std::atomic<uint64_t> ready{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  int n = dev < 64 ? known[dev][S].load(std::memory_order_relaxed) : 0;
-  if (n == 0) {
-    e = allow_smem(kernel, C::SMEM_BYTES, ready);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(S * 64);
-    cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    n = std::max(n, 1);
-    if (dev < 64) known[dev][S].store(n, std::memory_order_relaxed);
-  }
-  *out = n;
-  return cudaSuccess;
+  const cudaError_t e = allow_smem(kernel, C::SMEM_BYTES, ready);
+  return e == cudaSuccess ? clusters_at_once(kernel, kTileThreads, C::SMEM_BYTES, S, known, out) : e;
 }
 
 // The tiling for many tokens: the least of these estimates (us), fitted to 40

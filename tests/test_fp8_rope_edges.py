@@ -682,3 +682,12 @@ def test_rope_refuses_one_memory_for_queries_and_keys(zq):
     # no keys, no tokens: nothing to refuse
     assert rope_call(zq, q=dict(i=A, o=A), k=dict(i=A, o=A), T=0) == zq.ZQ_OK
     assert rope_call(zq, q=dict(n=0), k=dict(n=0)) == zq.ZQ_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 16, 40])
+@pytest.mark.parametrize("N,K", [(5120, 5120), (2048, 12288), (8192, 4096), (1024, 24576), (4104, 8208), (24576, 1024),
+                                 (20488, 272)])
+def test_gemm_weight_rows_of_large_matrices(zq, T, N, K):
+    """Two CTAs per SM, in clusters of one to eight."""
+    check_gemm_on_device(zq, T, K, N, torch.bfloat16 if T == 16 else torch.float16)
