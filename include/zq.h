@@ -344,7 +344,8 @@ zq_status zq_bias_act_quant_fp8(const void* X, int dtype, const void* bias, int 
  *     d[t][o][b] = sum over the k of block b of xq[t][k] * wq[o][k].
  *     d is summed by the tensor cores in fp32; the blocks are added in fp32,
  *     in an order that the sizes alone set (the same inputs give the same
- *     bits); one rounding to `dtype` at the end.
+ *     bits); one rounding to `dtype` at the end.  s_x * s_w is one fp32
+ *     product: below 2^-126 it loses digits, and past 2^128 it is infinite.
  * No workspace: calls on different streams, and replayed graphs of them, may
  * overlap.
  * Requirements: T >= 0 (T == 0 is a no-op), N >= 8, N % 8 == 0,
@@ -384,8 +385,9 @@ zq_status zq_gemm_fp8(const void* Xq, const float* s_x, const void* Wq, const fl
  *   layout     ZQ_ROPE_HALF pairs values i and i + R/2 (GPT-NeoX),
  *              ZQ_ROPE_INTERLEAVED 2i and 2i + 1 (GPT-J), with frequency i.
  *              (a, b) -> (a cos - b sin, b cos + a sin) * scale; the angle
- *              position * inv_freq[i] is reduced in 64 bits, so far positions
- *              are as exact as near ones.
+ *              position * inv_freq[i] is reduced in 64 bits: angles up to 2^27
+ *              radians are as exact as near ones (half a step of fp32), one of
+ *              2^31 is within 2^-20.
  *   Values behind R get the norm alone.
  * Requirements: T >= 0, 8 <= D <= 256, D % 8 == 0, 0 <= R <= D, R even
  * (R % 4 == 0 for ZQ_ROPE_HALF), head counts >= 0, strides >= 0 and multiples

@@ -55,8 +55,8 @@ constexpr int kRowsCtas = 4;  // CTAs per SM: 64 registers per thread
 // Blocks are numbered row by row, so neighbouring lanes read neighbouring
 // pieces.  The last block of a row is short when K is no multiple of 128: its
 // missing lanes hold 0.  As they are, 4096 x 6144 take 13.9 us (5.4 TB/s, 0.83 of
-// a copy); with a GeLU 1531 x 16384 take 22.9, bound by 21.5 instructions per
-// value (issue slots 72% taken, the special-function unit half).
+// a copy); with a GeLU 1531 x 16384 take 24.5, bound by 23 instructions per
+// value (issue slots 73% taken, the special-function unit half).
 template <typename E, int ACT>
 __global__ void __launch_bounds__(256, kRowsCtas)
     fp8_rows_kernel(const E* __restrict__ X, const E* __restrict__ bias, int K, unsigned kblocks,

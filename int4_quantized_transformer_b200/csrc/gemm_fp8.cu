@@ -109,6 +109,9 @@ cudaError_t clusters_at_once(K* kernel, int threads, int smem, int S,
 // cluster share rows along K and exchange their sums through distributed
 // shared memory: rank r ends with every token c with c mod S == r, added in
 // rank order.
+// At 48 tokens, weight rows against tiles (us): 24576 x 6144 33.9 / 35.0, 6144 x
+// 24576 37.9 / 42.5, 6144 x 6144 15.6 / 15.6, 12288 x 4096 17.8 / 16.4, 4096 x 4096
+// 11.7 / 9.9; from 65 on only tiles can.
 constexpr int kRowsMaxTokens = 64;
 constexpr int kRowsAccWarps = 8;
 constexpr int kRowsThreads = 32 * (4 + kRowsAccWarps);  // copies, MMAs, scales (two warps)
@@ -526,8 +529,8 @@ cudaError_t launch_rows_any(const Fp8Params& p, cudaStream_t st) {
 //
 // 4096 x 6144 x 18432 takes 412 us alone (2.25 PFLOP/s) and 490 to 505 in a row,
 // where power lowers the clock: 628 thousand cycles, of which the MMAs alone
-// are 383.  Copies of it with parts left out, when it took 652: without the FMAs
-// 543, without the output's stores 617, without both 470, without the scales'
+// are 383.  Copies of an earlier state that took 652, with parts left out: without
+// the FMAs 543, without the output's stores 617, without both 470, without the scales'
 // copies too 413.  A block's sums wait for their MMAs, are loaded, added, and handed
 // back across the pair, with two buffers to cover that: the FMAs (256 cycles per
 // block and scheduler at best, 512 the MMAs) lengthen it, the loads from tensor

@@ -155,9 +155,11 @@ __device__ __forceinline__ Tile tile_of(const RopeParams& p) {
 __device__ __forceinline__ void tile_angles(const RopeParams& p, const Tile& t, float* cs, float* sn,
                                             int* pos) {
   const int half = p.R / 2;
-  // The angle in turns, reduced to half a turn on either side in 64 bits (the
-  // product of a position and an fp32 frequency is exact there), so that far
-  // positions lose nothing before the fp32 sine and cosine.
+  // The angle in turns, reduced to half a turn on either side in 64 bits, before
+  // the fp32 sine and cosine.  The product of position and frequency (exact for
+  // positions up to 2^29), 1 / (2 pi) and their product are off by at most 2.8 *
+  // 2^-53 of the angle: below half a step of fp32 up to 2^27 radians, 2^-20.5
+  // radians at 2^31.
   for (int i = threadIdx.x; i < t.tokens * t.row; i += blockDim.x) {
     const int k = i / t.row, f = i - k * t.row;
     float s = 0.0f, c = 1.0f;
@@ -268,8 +270,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   }
 }
 
-// With a norm; bound by 16 instructions per value in one chain from the load
-// to the store, at 24 warps per SM: 3.7 to 4.9 TB/s at many tokens.  (On pairs
+// With a norm; bound by the latency of a token's one chain from the load to the
+// store (16 instructions per value, two reductions with a LayerNorm) at 24 warps
+// per SM, whose issue slots are 62% taken: 3.7 to 4.9 TB/s at many tokens.  (On pairs
 // of fp32 it was slower: 17.6 us instead of 15.1 for 2048 tokens of 32 heads of
 // 256.)  2^k lanes have a head, NU units to a lane.  Units behind the
 // rotated ones have 2 TAIL neighbouring values of the rest (in the neighbours
